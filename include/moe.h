@@ -217,6 +217,101 @@ moe_status moe_layer_forward_noalloc(const moe_layer_desc *desc, const void *x, 
                                      const moe_layer_weights *w, int32_t *idx_out,
                                      float *gate_w_out, void *out, void *stream);
 
+/* ---- operators around the layer -------------------------------------------------------
+ * What a block needs next to its MoE layer: the norm in front of it, the dense
+ * FFN of the blocks without experts ("Guide Complet de Colibri", table "Points
+ * techniques cles", router row: the first three layers are dense), and routing
+ * with groups.  These calls take no context: they only enqueue kernels on
+ * `stream` of the current device, allocate nothing, keep nothing from one call
+ * to the next and need no workspace; any number may run at once on different
+ * streams.  They may be captured into a HIP graph.
+ * A leading dimension ld is the distance between rows in elements (at least the
+ * row's length); pointers need only their element's alignment.  T is in
+ * [0, 2^20]; T == 0 does nothing.  Inputs and outputs must not overlap except
+ * where stated.  Errors of each: E_INVAL (a bad
+ * argument; nothing was enqueued), E_UNSUPPORTED (not a gfx950 device), E_HIP.
+ *
+ * Codes: int8 with one fp32 scale per row, by the rule of the layer's own
+ * activations: a = max |v|, s = a/127, q = clamp(rint(v * (127/a)), -127, 127),
+ * in fp32; a row of zeros gives s = 0 and q = 0.  A row holding a NaN or an
+ * infinity gives s = NaN and q = 0, so what is made from it is NaN too.
+ *
+ * moe_rmsnorm_quant: for T rows of H (1 <= H <= 2^20)
+ *   h = x + residual (fp32; h = x when residual is NULL),
+ *   v = (h * r) * gamma,  r = fp32(1/sqrt(mean(h^2) + eps)), the sum in fp64,
+ * with any of these outputs, NULL for those not wanted: h_out [T,H] (of the
+ * residual's dtype; the norm reads the unrounded sum), y_out [T,H] bf16 (v
+ * rounded to nearest even: the input of moe_router_topk and moe_layer_forward),
+ * q [T,H] with s [T] (the input of moe_linear_int8).  x and residual are
+ * MOE_DT_F32 or MOE_DT_BF16; gamma [H] fp32, NULL for ones.  h_out may be the
+ * residual or x itself (same dtype and ld); without a residual, h_out takes
+ * x's dtype as res_dtype.  eps > 0. */
+moe_status moe_rmsnorm_quant(const void *x, int32_t x_dtype, int64_t ldx, const void *residual,
+                             int32_t res_dtype, int64_t ldr, const float *gamma, int32_t T,
+                             int32_t H, float eps, void *h_out, int64_t ldh, void *y_out,
+                             int64_t ldy, int8_t *q, int64_t ldq, float *s, void *stream);
+
+/* moe_swiglu_quant: gu [T,2F] holds per row F gate values G, then F up values U
+ * (the product of moe_linear_int8 with the gate rows above the up rows);
+ * v = G/(1+exp(-G)) * U in fp32, given as codes q [T,F] with s [T], and as
+ * bf16 in y_out [T,F] unless that is NULL (q and s may be NULL instead).
+ * 1 <= F <= 2^20. */
+moe_status moe_swiglu_quant(const void *gu, int32_t gu_dtype, int64_t ld, int32_t T, int32_t F,
+                            void *y_out, int64_t ldy, int8_t *q, int64_t ldq, float *s,
+                            void *stream);
+
+/* moe_linear_int8: out[t,n] = (float(sum_k q[t,k]*w[n,k]) * s[t]) * ws[n] + bias[n]
+ * for q [T,K] with row scales s [T] and weights w [N,K] with channel scales
+ * ws [N]; bias [N] may be NULL.  Codes are any int8 values; the sum is exact
+ * (int32, 1 <= K <= 131071) and the rest fp32 in that order, so the bits of out
+ * depend on nothing but the inputs.  out is MOE_DT_F32 or MOE_DT_BF16 (rounded
+ * to nearest even).  1 <= N <= 2^20. */
+moe_status moe_linear_int8(const int8_t *q, int64_t ldq, const float *s, int32_t T,
+                           const int8_t *w, int64_t ldw, const float *ws, const float *bias,
+                           int32_t N, int32_t K, void *out, int32_t out_dtype, int64_t ldo,
+                           void *stream);
+
+/* Routing with groups (the family's larger models keep a token's experts within
+ * a few groups).  For logits l [T,E]:
+ *   p = 1/(1+exp(-l)) (MOE_SCORE_SIGMOID) or exp(l - max)/sum (MOE_SCORE_SOFTMAX,
+ *   over all E); c = p + bias (the bias only steers the choice).
+ * The E experts form n_group groups of E/n_group neighbours.  A group's score is
+ * the sum of its group_best (1 or 2) largest c; the topk_group groups with the
+ * largest scores stay, ties to the lower group.  idx [T,k] int32 = the k experts
+ * of those groups with the largest c, in rank order, ties to the lower index;
+ * gate_w [T,k] fp32 = p[idx] * scale, divided by sum(p[idx]) if renorm (all 0
+ * where that sum is 0).  A NaN logit counts as p = 0, c = -inf; a softmax row
+ * whose logits are all -inf as p = 0; a +inf logit shares the row's whole
+ * probability with its equals.  Every row gets k distinct experts.
+ *  n_experts E in [1, 1024], top_k k in [1, 32], n_group in [1, 64] a divisor of
+ *  E, topk_group in [1, n_group], k <= topk_group * E/n_group, group_best 1 or 2
+ *  (2 only with at least 2 experts a group), renorm 0 or 1, scale finite and >= 0.
+ * moe_route_select: from logits of MOE_DT_F32 or MOE_DT_BF16, scores in fp32;
+ * bias [E] fp32 or NULL.  No context.
+ * moe_router_topk_grouped: moe_router_topk with this choice instead of its own:
+ * x [T,H] bf16 and w->router_w give the fp64 logits (the kernels and the
+ * workspace of ctx), w->router_bias the bias (NULL for none), scores in fp64.  desc's n_experts must
+ * be the layer's; top_k is desc's own, but idx feeds moe_expert_ffn only where it
+ * equals the layer's.  T in [0, max_tokens]. */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+typedef struct moe_route_desc {
+    int32_t n_experts;
+    int32_t top_k;
+    int32_t score;
+    int32_t n_group;
+    int32_t topk_group;
+    int32_t group_best;
+    int32_t renorm;
+    float   scale;
+} moe_route_desc;
+moe_status moe_route_select(const moe_route_desc *desc, const void *logits, int32_t logit_dtype,
+                            int64_t ld, const float *bias, int32_t T, int32_t *idx,
+                            float *gate_w, void *stream);
+moe_status moe_router_topk_grouped(moe_ctx *ctx, const moe_route_desc *desc, const void *x,
+                                   int32_t T, const moe_layer_weights *w, int32_t *idx,
+                                   float *gate_w, void *stream);
+
 /* ---- expert cache ---------------------------------------------------------------
  * Source: "Guide Complet de Colibri", sections "Qu'est-ce que Colibri ?" (LRU
  * expert cache, experts loaded on demand) and "Router-Lookahead prefetch" (the

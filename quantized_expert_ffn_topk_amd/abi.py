@@ -23,6 +23,7 @@ CACHE_GLOBAL_LRU, CACHE_PER_LAYER_LRU = 0, 1
 CACHE_BACKEND_HIP, CACHE_BACKEND_HOST = 0, 1
 STAGE_DEMAND, STAGE_PREFETCH, STAGE_PREFETCH_IDLE = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 
 _NAMES = {OK: "OK", E_INVAL: "E_INVAL", E_UNSUPPORTED: "E_UNSUPPORTED", E_NOMEM: "E_NOMEM",
           E_HIP: "E_HIP", E_CAPACITY: "E_CAPACITY"}
@@ -43,6 +44,12 @@ class moe_layer_desc(C.Structure):
 class moe_layer_weights(C.Structure):
     _fields_ = [("router_w", C.c_void_p), ("router_bias", C.c_void_p),
                 ("expert_ptrs", C.c_void_p), ("shared", C.c_void_p)]
+
+
+class moe_route_desc(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32),
+                ("n_group", C.c_int32), ("topk_group", C.c_int32), ("group_best", C.c_int32),
+                ("renorm", C.c_int32), ("scale", C.c_float)]
 
 
 class moe_cache_desc(C.Structure):
@@ -83,7 +90,7 @@ def lib():
 
 
 def _declare(L):
-    vp, i32, st = C.c_void_p, C.c_int32, C.c_int32
+    vp, i32, i64, f32, st = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_int32
     P = C.POINTER
     sig = {
         "moe_ctx_create": (st, [i32, P(moe_layer_desc), i32, P(vp)]),
@@ -99,6 +106,13 @@ def _declare(L):
         "moe_layer_forward": (st, [vp, vp, i32, P(moe_layer_weights), vp, i32, vp, vp, vp, vp]),
         "moe_layer_forward_noalloc": (st, [P(moe_layer_desc), vp, i32, P(moe_layer_weights), vp,
                                            vp, vp, vp]),
+        "moe_rmsnorm_quant": (st, [vp, i32, i64, vp, i32, i64, vp, i32, i32, f32, vp, i64, vp, i64,
+                                   vp, i64, vp, vp]),
+        "moe_swiglu_quant": (st, [vp, i32, i64, i32, i32, vp, i64, vp, i64, vp, vp]),
+        "moe_linear_int8": (st, [vp, i64, vp, i32, vp, i64, vp, vp, i32, i32, vp, i32, i64, vp]),
+        "moe_route_select": (st, [P(moe_route_desc), vp, i32, i64, vp, i32, vp, vp, vp]),
+        "moe_router_topk_grouped": (st, [vp, P(moe_route_desc), vp, i32, P(moe_layer_weights), vp,
+                                         vp, vp]),
         "moe_cache_create": (st, [P(moe_cache_desc), P(vp)]),
         "moe_cache_destroy": (None, [vp]),
         "moe_cache_stage": (st, [vp, i32, vp, i32, i32, vp, vp]),
@@ -232,6 +246,33 @@ def moe_layer_forward_noalloc(desc, x, T, weights, idx_out, gate_w_out, out, str
     check(lib().moe_layer_forward_noalloc(C.byref(desc), addr(x), T, C.byref(weights),
                                           addr(idx_out), addr(gate_w_out), addr(out),
                                           stream_handle(stream)))
+
+
+def moe_rmsnorm_quant(x, x_dtype, ldx, residual, res_dtype, ldr, gamma, T, H, eps, h_out, ldh,
+                      y_out, ldy, q, ldq, s, stream=None):
+    check(lib().moe_rmsnorm_quant(addr(x), x_dtype, ldx, addr(residual), res_dtype, ldr, addr(gamma),
+                                  T, H, eps, addr(h_out), ldh, addr(y_out), ldy, addr(q), ldq,
+                                  addr(s), stream_handle(stream)))
+
+
+def moe_swiglu_quant(gu, gu_dtype, ld, T, F, y_out, ldy, q, ldq, s, stream=None):
+    check(lib().moe_swiglu_quant(addr(gu), gu_dtype, ld, T, F, addr(y_out), ldy, addr(q), ldq,
+                                 addr(s), stream_handle(stream)))
+
+
+def moe_linear_int8(q, ldq, s, T, w, ldw, ws, bias, N, K, out, out_dtype, ldo, stream=None):
+    check(lib().moe_linear_int8(addr(q), ldq, addr(s), T, addr(w), ldw, addr(ws), addr(bias), N, K,
+                                addr(out), out_dtype, ldo, stream_handle(stream)))
+
+
+def moe_route_select(desc, logits, logit_dtype, ld, bias, T, idx, gate_w, stream=None):
+    check(lib().moe_route_select(C.byref(desc), addr(logits), logit_dtype, ld, addr(bias), T,
+                                 addr(idx), addr(gate_w), stream_handle(stream)))
+
+
+def moe_router_topk_grouped(ctx, desc, x, T, weights, idx, gate_w, stream=None):
+    check(lib().moe_router_topk_grouped(ctx, C.byref(desc), addr(x), T, C.byref(weights), addr(idx),
+                                        addr(gate_w), stream_handle(stream)))
 
 
 def moe_cache_create(desc):

@@ -1,0 +1,547 @@
+// kernels_rows.hip -- row operators around the MoE layer on gfx950: the RMS
+// norm with the residual's addition, and SwiGLU, both with int8 output (codes
+// and one scale per row) beside or instead of bf16.
+#include "ops_common.h"
+
+#include <cmath>
+
+namespace moe {
+
+// ---------------------------------------------------------------------------
+// Sources of a row's fp32 values.
+// ---------------------------------------------------------------------------
+template <typename XT, typename RT>
+struct NormArgs {
+    const XT *x;
+    const RT *res;             // NULL: none
+    const float *gamma;        // NULL: ones
+    RT *h;                     // NULL: not wanted
+    int64_t ldx, ldr, ldh;
+    float eps;
+};
+template <typename XT>
+struct SwigluArgs {
+    const XT *gu;
+    int64_t ld;
+};
+struct RowOut {
+    bf16_t *y;                 // NULL: not wanted
+    int8_t *q;                 // NULL: not wanted (then s too)
+    float *s;
+    int64_t ldy, ldq;
+    int T, n;
+};
+
+// silu(g)*u in fp32, from E = exp(-|g|) <= 1 so that nothing overflows:
+// g*u/(1+E) for g >= 0, g*u*E/(1+E) for g < 0.  E = 2^t with t = -|g|*log2(e)
+// as a rounded product and its remainder, so that the exponent's rounding does
+// not grow with |g|; the reciprocal is the hardware's (one unit in the last
+// place), of a number in [1,2].  Past |g| = 200 E is 0 either way.
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    const float L2E = 1.44269502f, L2E_LO = 1.92596303e-8f;   // log2(e) = L2E + L2E_LO
+    const float a = fminf(fabsf(g), 200.0f);
+    const float t = -a * L2E;
+    const float r = fmaf(-a, L2E, -t) - a * L2E_LO;
+    float e = __builtin_exp2f(t);
+    e = fmaf(e, r * 0.693147181f, e);
+    const float d = __builtin_amdgcn_rcpf(1.0f + e);
+    return g * ((g < 0.0f) ? e * d : d) * u;
+}
+
+// ---------------------------------------------------------------------------
+// One row by NT threads, NV vectors of 8 values per thread (8*NT*NV >= n), the
+// row in registers between its one read and its writes.  A thread's vector i
+// covers values [col, col+8), col = 8*(lane + NT*i); one that passes the row's
+// end reads (and writes again, with the same values) the row's last 8 values,
+// of which `first` counts those that are not its own in the sum.  Rows shorter
+// than 8 are read value by value.
+// NT = 64: a wave per row, four rows per block, no barrier.
+// ---------------------------------------------------------------------------
+template <int NT>
+__device__ __forceinline__ double row_sum_d(double v, double *red)
+{
+    v = wave_sum_d(v);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0)
+            red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w)
+            v += red[w];
+    }
+    return v;
+}
+
+template <int NT>
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v, uint32_t *red)
+{
+    v = wave_max_u32(v);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0)
+            red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w)
+            v = max(v, red[w]);
+    }
+    return v;
+}
+
+// scale and multiplier of a row whose largest magnitude has the fp32 bits m.
+// Rows below 2^-96 are multiplied by 2^64 first (exact), so that 127/max stays
+// finite.
+__device__ __forceinline__ void row_scale(uint32_t m, float *s, float *pre, float *inv)
+{
+    const float a = __uint_as_float(m);
+    *s = a / 127.0f;
+    *pre = (a < 0x1p-96f) ? 0x1p64f : 1.0f;
+    *inv = (m == 0u) ? 0.0f : 127.0f / (a * *pre);
+    if (m >= 0x7f800000u) {
+        *s = __uint_as_float(0x7fc00000u);
+        *pre = *inv = 0.0f;
+    }
+}
+
+// rint(v*pre*inv) clamped, as the low byte; 0 throughout where inv is 0 (a row
+// of zeros, or one with a NaN or an infinity, whose products may be NaN)
+__device__ __forceinline__ uint32_t code(float v, float pre, float inv)
+{
+    const float r = fminf(fmaxf(rintf((v * pre) * inv), -127.0f), 127.0f);
+    return (inv == 0.0f) ? 0u : (uint32_t)(int)r & 0xffu;
+}
+
+template <int NT, int NV, typename LoadFn, typename MidFn>
+__device__ __forceinline__ void row_body(const RowOut &o, int t, int lane, bool live,
+                                         uint32_t *red, LoadFn load, MidFn mid)
+{
+    const int n = o.n;
+    float v[NV][8];
+    int c[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        c[i] = max(0, min(8 * (lane + NT * i), n - 8));
+    load(v, c);
+    mid(v, c);
+    const bool tiny = n < 8;
+    if (o.y && live) {
+        bf16_t *yr = o.y + (int64_t)t * o.ldy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (8 * (lane + NT * i) >= n)
+                continue;
+            if (!tiny) {
+                store8(yr + c[i], v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < n)
+                        store1(yr + j, v[i][j]);
+            }
+        }
+    }
+    if (!o.q)
+        return;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
+    m = row_max_u32<NT>(m, red);
+    float s, pre, inv;
+    row_scale(m, &s, &pre, &inv);
+    if (!live)
+        return;
+    int8_t *qr = o.q + (int64_t)t * o.ldq;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (8 * (lane + NT * i) >= n)
+            continue;
+        uint32_t d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            d[j] = code(v[i][j], pre, inv);
+        if (!tiny) {
+            bytes8_a1 b;
+            b.d[0] = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
+            b.d[1] = d[4] | d[5] << 8 | d[6] << 16 | d[7] << 24;
+            *reinterpret_cast<bytes8_a1 *>(qr + c[i]) = b;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n)
+                    qr[j] = (int8_t)d[j];
+        }
+    }
+    if (lane == 0)
+        o.s[t] = s;
+}
+
+// 8 values at column c of a row of n (value by value where n < 8, zeros past n)
+template <typename XT>
+__device__ __forceinline__ void row_load8(const XT *p, int c, int n, float (&v)[8])
+{
+    if (n >= 8) {
+        load8(p + c, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = (j < n) ? to_f32(p[j]) : 0.0f;
+    }
+}
+
+template <int NT>
+constexpr int rows_per_block()
+{
+    return NT == 64 ? 4 : 1;
+}
+template <int NT>
+constexpr int block_threads()
+{
+    return NT == 64 ? 256 : NT;
+}
+
+template <int NT, int NV, typename XT, typename RT>
+__global__ __launch_bounds__(block_threads<NT>()) void rmsnorm_kernel(NormArgs<XT, RT> a, RowOut o)
+{
+    __shared__ double red_d[NT / 64];
+    __shared__ uint32_t red_m[NT / 64];
+    const int lane = (NT == 64) ? threadIdx.x & 63 : threadIdx.x;
+    const int row = (NT == 64) ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const bool live = row < o.T;
+    const int t = live ? row : o.T - 1;            // a wave past the rows repeats the last, stores nothing
+    const int n = o.n;
+    row_body<NT, NV>(
+        o, t, lane, live, red_m,
+        [&](float (&v)[NV][8], const int (&c)[NV]) {
+            const XT *xr = a.x + (int64_t)t * a.ldx;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                row_load8(xr, c[i], n, v[i]);
+            if (a.res) {
+                const RT *rr = a.res + (int64_t)t * a.ldr;
+                float r[NV][8];
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    row_load8(rr, c[i], n, r[i]);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[i][j] += r[i][j];
+            }
+        },
+        [&](float (&v)[NV][8], const int (&c)[NV]) {
+            double ss = 0.0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int col = 8 * (lane + NT * i);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const double d = (c[i] + j >= col) ? (double)v[i][j] : 0.0;
+                    ss = fma(d, d, ss);
+                }
+            }
+            ss = row_sum_d<NT>(ss, red_d);
+            const float r = (float)(1.0 / sqrt(ss / (double)n + (double)a.eps));
+            if (a.h && live) {
+                RT *hr = a.h + (int64_t)t * a.ldh;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (8 * (lane + NT * i) >= n)
+                        continue;
+                    if (n >= 8) {
+                        store8(hr + c[i], v[i]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < n)
+                                store1(hr + j, v[i][j]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float g[8];
+                if (a.gamma)
+                    row_load8(a.gamma, c[i], n, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float y = v[i][j] * r;
+                    v[i][j] = a.gamma ? y * g[j] : y;
+                }
+            }
+        });
+}
+
+template <int NT, int NV, typename XT>
+__global__ __launch_bounds__(block_threads<NT>()) void swiglu_kernel(SwigluArgs<XT> a, RowOut o)
+{
+    __shared__ uint32_t red_m[NT / 64];
+    const int lane = (NT == 64) ? threadIdx.x & 63 : threadIdx.x;
+    const int row = (NT == 64) ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const bool live = row < o.T;
+    const int t = live ? row : o.T - 1;
+    const int n = o.n;
+    row_body<NT, NV>(
+        o, t, lane, live, red_m,
+        [&](float (&v)[NV][8], const int (&c)[NV]) {
+            const XT *gr = a.gu + (int64_t)t * a.ld;
+            const XT *ur = gr + n;
+            float u[NV][8];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                row_load8(gr, c[i], n, v[i]);
+                row_load8(ur, c[i], n, u[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] = silu_mul(v[i][j], u[i][j]);
+        },
+        [&](float (&)[NV][8], const int (&)[NV]) {});
+}
+
+// ---------------------------------------------------------------------------
+// Rows too long for the registers (n > 32768): 1024 threads read the row again
+// for each step; every value is read and written by one thread, the writes in
+// the last step, so h_out may be an input here too.
+// ---------------------------------------------------------------------------
+template <typename XT, typename RT>
+__global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs<XT, RT> a, RowOut o)
+{
+    __shared__ double red_d[16];
+    __shared__ uint32_t red_m[16];
+    const int t = blockIdx.x, n = o.n;
+    const XT *xr = a.x + (int64_t)t * a.ldx;
+    const RT *rr = a.res ? a.res + (int64_t)t * a.ldr : nullptr;
+    auto value = [&](int i) {
+        const float v = to_f32(xr[i]);
+        return rr ? v + to_f32(rr[i]) : v;
+    };
+    double ss = 0.0;
+    for (int i = threadIdx.x; i < n; i += 1024) {
+        const double d = (double)value(i);
+        ss = fma(d, d, ss);
+    }
+    ss = row_sum_d<1024>(ss, red_d);
+    const float r = (float)(1.0 / sqrt(ss / (double)n + (double)a.eps));
+    auto normed = [&](float h, int i) {
+        const float y = h * r;
+        return a.gamma ? y * a.gamma[i] : y;
+    };
+    float s = 0.0f, pre = 0.0f, inv = 0.0f;
+    if (o.q) {
+        uint32_t m = 0u;
+        for (int i = threadIdx.x; i < n; i += 1024)
+            m = max(m, __float_as_uint(normed(value(i), i)) & 0x7fffffffu);
+        row_scale(row_max_u32<1024>(m, red_m), &s, &pre, &inv);
+    }
+    for (int i = threadIdx.x; i < n; i += 1024) {
+        const float h = value(i);
+        const float v = normed(h, i);
+        if (a.h)
+            store1(a.h + (int64_t)t * a.ldh + i, h);
+        if (o.y)
+            store1(o.y + (int64_t)t * o.ldy + i, v);
+        if (o.q)
+            o.q[(int64_t)t * o.ldq + i] = (int8_t)code(v, pre, inv);
+    }
+    if (o.q && threadIdx.x == 0)
+        o.s[t] = s;
+}
+
+template <typename XT>
+__global__ __launch_bounds__(1024) void swiglu_long_kernel(SwigluArgs<XT> a, RowOut o)
+{
+    __shared__ uint32_t red_m[16];
+    const int t = blockIdx.x, n = o.n;
+    const XT *gr = a.gu + (int64_t)t * a.ld;
+    auto value = [&](int i) { return silu_mul(to_f32(gr[i]), to_f32(gr[n + i])); };
+    float s = 0.0f, pre = 0.0f, inv = 0.0f;
+    if (o.q) {
+        uint32_t m = 0u;
+        for (int i = threadIdx.x; i < n; i += 1024)
+            m = max(m, __float_as_uint(value(i)) & 0x7fffffffu);
+        row_scale(row_max_u32<1024>(m, red_m), &s, &pre, &inv);
+    }
+    for (int i = threadIdx.x; i < n; i += 1024) {
+        const float v = value(i);
+        if (o.y)
+            store1(o.y + (int64_t)t * o.ldy + i, v);
+        if (o.q)
+            o.q[(int64_t)t * o.ldq + i] = (int8_t)code(v, pre, inv);
+    }
+    if (o.q && threadIdx.x == 0)
+        o.s[t] = s;
+}
+
+// ---------------------------------------------------------------------------
+// Shapes: the fewest threads that hold the row in at most 4 vectors each.
+// ---------------------------------------------------------------------------
+template <int NT, typename F>
+static void with_nv(int n, F &&f)
+{
+    const int nv = (n + 8 * NT - 1) / (8 * NT);
+    if (nv <= 1)
+        f(std::integral_constant<int, 1>());
+    else if (nv == 2)
+        f(std::integral_constant<int, 2>());
+    else if (nv == 3)
+        f(std::integral_constant<int, 3>());
+    else
+        f(std::integral_constant<int, 4>());
+}
+
+template <typename F>
+static void with_shape(int n, F &&f)
+{
+    if (n <= 64 * 32)
+        with_nv<64>(n, [&](auto nv) { f(std::integral_constant<int, 64>(), nv); });
+    else if (n <= 256 * 32)
+        with_nv<256>(n, [&](auto nv) { f(std::integral_constant<int, 256>(), nv); });
+    else
+        with_nv<1024>(n, [&](auto nv) { f(std::integral_constant<int, 1024>(), nv); });
+}
+
+constexpr int ROW_REG_MAX = 32768;
+
+static unsigned row_grid(int T, int nt)
+{
+    return nt == 64 ? (unsigned)(((int64_t)T + 3) / 4) : (unsigned)T;
+}
+
+template <typename XT, typename RT>
+static void enqueue_norm(const NormArgs<XT, RT> &a, const RowOut &o, hipStream_t st)
+{
+    if (o.n > ROW_REG_MAX) {
+        launch(rmsnorm_long_kernel<XT, RT>, (unsigned)o.T, 1024, 0, st, a, o);
+        return;
+    }
+    with_shape(o.n, [&](auto nt, auto nv) {
+        launch(rmsnorm_kernel<nt(), nv(), XT, RT>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
+    });
+}
+
+template <typename XT>
+static void enqueue_swiglu(const SwigluArgs<XT> &a, const RowOut &o, hipStream_t st)
+{
+    if (o.n > ROW_REG_MAX) {
+        launch(swiglu_long_kernel<XT>, (unsigned)o.T, 1024, 0, st, a, o);
+        return;
+    }
+    with_shape(o.n, [&](auto nt, auto nv) {
+        launch(swiglu_kernel<nt(), nv(), XT>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
+    });
+}
+
+static moe_status check_rows(int32_t T, int32_t n, const char *name, const void *y, int64_t ldy,
+                             const void *q, int64_t ldq, const void *s)
+{
+    if (T < 0 || T > (1 << 20))
+        return fail(MOE_E_INVAL, "T=%d out of range [0, 2^20]", T);
+    if (n < 1 || n > (1 << 20))
+        return fail(MOE_E_INVAL, "%s=%d must be in [1, 2^20]", name, n);
+    if ((q == nullptr) != (s == nullptr))
+        return fail(MOE_E_INVAL, "q and s go together");
+    if (y && ldy < n)
+        return fail(MOE_E_INVAL, "ldy=%lld is below %s=%d", (long long)ldy, name, n);
+    if (q && ldq < n)
+        return fail(MOE_E_INVAL, "ldq=%lld is below %s=%d", (long long)ldq, name, n);
+    if (!ops_aligned(y, 2) || !ops_aligned(s, 4))
+        return fail(MOE_E_INVAL, "y_out and s must be aligned to their elements");
+    return MOE_OK;
+}
+
+static size_t dtype_size(int32_t dt)
+{
+    return dt == MOE_DT_F32 ? 4 : 2;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_rmsnorm_quant(const void *x, int32_t x_dtype, int64_t ldx,
+                                        const void *residual, int32_t res_dtype, int64_t ldr,
+                                        const float *gamma, int32_t T, int32_t H, float eps,
+                                        void *h_out, int64_t ldh, void *y_out, int64_t ldy,
+                                        int8_t *q, int64_t ldq, float *s, void *stream)
+{
+    moe_status st = check_rows(T, H, "H", y_out, ldy, q, ldq, s);
+    if (st)
+        return st;
+    if (!ops_dtype_ok(x_dtype))
+        return fail(MOE_E_INVAL, "unknown x_dtype %d", x_dtype);
+    if ((residual || h_out) && !ops_dtype_ok(res_dtype))
+        return fail(MOE_E_INVAL, "unknown res_dtype %d", res_dtype);
+    if (!residual && h_out && res_dtype != x_dtype)
+        return fail(MOE_E_INVAL, "without a residual h_out has x's dtype");
+    if (!(eps > 0.0f) || !(eps < INFINITY))
+        return fail(MOE_E_INVAL, "eps must be finite and > 0");
+    if (!y_out && !q && !h_out)
+        return fail(MOE_E_INVAL, "no output is wanted");
+    if (T == 0)
+        return MOE_OK;
+    if (!x)
+        return fail(MOE_E_INVAL, "x is NULL");
+    if (ldx < H || (residual && ldr < H) || (h_out && ldh < H))
+        return fail(MOE_E_INVAL, "a leading dimension is below H=%d", H);
+    const size_t rs = dtype_size(res_dtype);
+    if (!ops_aligned(x, dtype_size(x_dtype)) || !ops_aligned(residual, rs) || !ops_aligned(h_out, rs) ||
+        !ops_aligned(gamma, 4))
+        return fail(MOE_E_INVAL, "x, residual, gamma and h_out must be aligned to their elements");
+    if ((st = ops_check_device()) != MOE_OK)
+        return st;
+    const RowOut o{static_cast<bf16_t *>(y_out), q, s, ldy, ldq, T, H};
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    auto with = [&](auto xt, auto rt) {
+        typedef decltype(xt) XT;
+        typedef decltype(rt) RT;
+        const NormArgs<XT, RT> a{static_cast<const XT *>(x), static_cast<const RT *>(residual), gamma,
+                                 static_cast<RT *>(h_out), ldx, ldr, ldh, eps};
+        enqueue_norm(a, o, hs);
+    };
+    const bool rf = (residual || h_out) ? res_dtype == MOE_DT_F32 : x_dtype == MOE_DT_F32;
+    if (x_dtype == MOE_DT_F32)
+        rf ? with(0.0f, 0.0f) : with(0.0f, bf16_t(0));
+    else
+        rf ? with(bf16_t(0), 0.0f) : with(bf16_t(0), bf16_t(0));
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "norm launch");
+}
+
+extern "C" moe_status moe_swiglu_quant(const void *gu, int32_t gu_dtype, int64_t ld, int32_t T,
+                                       int32_t F, void *y_out, int64_t ldy, int8_t *q, int64_t ldq,
+                                       float *s, void *stream)
+{
+    moe_status st = check_rows(T, F, "F", y_out, ldy, q, ldq, s);
+    if (st)
+        return st;
+    if (!ops_dtype_ok(gu_dtype))
+        return fail(MOE_E_INVAL, "unknown gu_dtype %d", gu_dtype);
+    if (!y_out && !q)
+        return fail(MOE_E_INVAL, "no output is wanted");
+    if (T == 0)
+        return MOE_OK;
+    if (!gu)
+        return fail(MOE_E_INVAL, "gu is NULL");
+    if (ld < 2 * (int64_t)F)
+        return fail(MOE_E_INVAL, "ld=%lld is below 2*F=%d", (long long)ld, 2 * F);
+    if (!ops_aligned(gu, dtype_size(gu_dtype)))
+        return fail(MOE_E_INVAL, "gu must be aligned to its elements");
+    if ((st = ops_check_device()) != MOE_OK)
+        return st;
+    const RowOut o{static_cast<bf16_t *>(y_out), q, s, ldy, ldq, T, F};
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (gu_dtype == MOE_DT_F32)
+        enqueue_swiglu(SwigluArgs<float>{static_cast<const float *>(gu), ld}, o, hs);
+    else
+        enqueue_swiglu(SwigluArgs<bf16_t>{static_cast<const bf16_t *>(gu), ld}, o, hs);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "SwiGLU launch");
+}

@@ -43,6 +43,14 @@ __device__ __forceinline__ v4i load_codes(const int8_t *row, int k, int K)
     return v;
 }
 
+// LDS written by lanes of a wave and read by others of the same wave
+__device__ __forceinline__ void wave_lds_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <typename OT>
 __device__ __forceinline__ void store_out(const LinArgs &a, int t, int n, int acc)
 {
@@ -53,91 +61,131 @@ __device__ __forceinline__ void store_out(const LinArgs &a, int t, int n, int ac
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: a stream of weights.  A block owns RT tiles of 16 weight rows and
-// TB tiles of 16 tokens; its W waves split K in steps of 64 codes and add their
-// exact sums through LDS.  v_mfma_i32_16x16x64_i8: lane l supplies 16 codes at
-// 16*(l/16) of weight row l%16 (A) and of token l%16 (B), straight from memory;
-// result register i is row 4*(l/16)+i, token l%16.
+// Few tokens: a stream of weights.  A block owns 16*RT weight rows and up to
+// 8*TC tokens; its W waves take stages of 128 codes of K in turn (so that a
+// block reads W*128 neighbouring bytes of each row) and add their exact sums
+// through LDS at the end.  A wave works alone: it reads 8 rows x 128 bytes per
+// load, neighbouring lanes on neighbouring bytes, passes them through LDS of
+// its own into fragments, and has the next stage's loads in flight meanwhile.
+// (Read from memory in the fragments' order, 16 rows x 64 bytes with
+// neighbouring lanes on different rows, the loads took a lookup for every
+// lane: 24 x 24576 x 6144 44 us, 28 like this.)
+// v_mfma_i32_16x16x64_i8: lane l supplies 16 codes at 16*(l/16) of weight row
+// l%16 (A) and of token l%16 (B); result register i is row 4*(l/16)+i, token
+// l%16.  LDS rows are swizzled as in the tiles below.
+// NT: weights read with the non-temporal hint.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ v4i load16(const int8_t *p)
 {
     const bytes16_a1 b = *reinterpret_cast<const bytes16_a1 *>(p);
     return v4i{(int)b.d[0], (int)b.d[1], (int)b.d[2], (int)b.d[3]};
 }
+__device__ __forceinline__ v4i load16_stream(const int8_t *p)
+{
+    typedef int v4i_a1 __attribute__((ext_vector_type(4), aligned(1)));
+    return __builtin_nontemporal_load((const __attribute__((address_space(1))) v4i_a1 *)p);
+}
 
-template <typename OT, int RT, int TB, int W, int U>
+template <typename OT, bool NT, int RT, int TC, int W>
 __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
 {
-    __shared__ v4i part[W][RT * TB][64];
+    constexpr int TB = (TC + 1) / 2;                     // 16-token tiles
+    constexpr int CW = 2 * RT, CP = CW + TC;             // 8-row pieces per stage: weights, all
+    constexpr int ST = 1024 * (CW + 2 * TB);             // LDS bytes per wave (whole token tiles;
+                                                         // what TC = 1 leaves unwritten is not stored)
+    static_assert(RT * TB * 1024 <= ST, "a wave's sums fit its LDS");
+    __shared__ __align__(128) uint8_t lds[W * ST];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * 16 * TB;
-    const int8_t *wr[RT], *qr[TB];
+    const int n0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * 8 * TC;
+    const int stages = a.K >> 7;
+    const int mine = (stages - wave + W - 1) / W;        // stages wave, wave + W, ...
+    const int8_t *src[CP];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-        wr[i] = a.w + (int64_t)min(n0 + 16 * i + (lane & 15), a.N - 1) * a.ldw + 16 * (lane >> 4);
+    for (int i = 0; i < CP; ++i) {
+        const int r = 8 * (i < CW ? i : i - CW) + (lane >> 3);
+        src[i] = (i < CW) ? a.w + (int64_t)min(n0 + r, a.N - 1) * a.ldw
+                          : a.q + (int64_t)min(t0 + r, a.T - 1) * a.ldq;
+        src[i] += 16 * (lane & 7) + 128 * wave;
+    }
+    uint8_t *slot = lds + wave * ST;
+    int put[2], at[2];                                   // of a piece's even and odd 8 rows; of K half u
 #pragma unroll
-    for (int i = 0; i < TB; ++i)
-        qr[i] = a.q + (int64_t)min(t0 + 16 * i + (lane & 15), a.T - 1) * a.ldq + 16 * (lane >> 4);
-    v4i acc[RT][TB];
+    for (int u = 0; u < 2; ++u) {
+        put[u] = 128 * (lane >> 3) + 16 * ((lane & 7) ^ (4 * u + (lane >> 4)));
+        at[u] = 128 * (lane & 15) + 16 * ((4 * u + (lane >> 4)) ^ ((lane >> 1) & 7));
+    }
+    v4i acc[RT][TB], reg[CP], wv[2][RT], qv[2][TB];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < TB; ++j)
             acc[i][j] = v4i{0, 0, 0, 0};
-    const int steps = a.K >> 6;
-    const int s_lo = (int)((int64_t)wave * steps / W), s_hi = (int)((int64_t)(wave + 1) * steps / W);
-    for (int s0 = s_lo; s0 < s_hi; s0 += U) {
-        v4i wv[U][RT], qv[U][TB];
+    auto fetch = [&]() {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = 64 * (int64_t)min(s0 + u, s_hi - 1);    // clamped: unconditional loads
+        for (int i = 0; i < CP; ++i) {
+            reg[i] = (NT && i < CW) ? load16_stream(src[i]) : load16(src[i]);
+            src[i] += 128 * W;
+        }
+    };
+    auto multiply = [&]() {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                wv[u][i] = load16(wr[i] + k);
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u][i], qv[u][j], acc[i][j], 0, 0, 0);
+    };
+    if (mine > 0)
+        fetch();
+    for (int i = 0; i < mine; ++i) {
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+            *reinterpret_cast<v4i *>(slot + 1024 * c + put[c & 1]) = reg[c];
+        if (i + 1 < mine)
+            fetch();
+        wave_lds_sync();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int k = 0; k < RT; ++k)
+                wv[u][k] = *reinterpret_cast<const v4i *>(slot + at[u] + 2048 * k);
 #pragma unroll
             for (int j = 0; j < TB; ++j)
-                qv[u][j] = load16(qr[j] + k);
+                qv[u][j] = *reinterpret_cast<const v4i *>(slot + at[u] + 1024 * CW + 2048 * j);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s0 + u < s_hi) {
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < TB; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u][i], qv[u][j], acc[i][j], 0, 0, 0);
-            }
-        }
+        wave_lds_sync();
+        multiply();
     }
-    if ((a.K & 63) && wave == W - 1) {
-        const int k = (steps << 6) + 16 * (lane >> 4);
-        v4i qv[TB];
+    if ((a.K & 127) && wave == stages % W) {             // the partial last stage
 #pragma unroll
-        for (int j = 0; j < TB; ++j)
-            qv[j] = load_codes(qr[j] - 16 * (lane >> 4), k, a.K);
+        for (int u = 0; u < 2; ++u) {
+            const int k = (stages << 7) + 64 * u + 16 * (lane >> 4);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const v4i wv = load_codes(wr[i] - 16 * (lane >> 4), k, a.K);
+            for (int i = 0; i < RT; ++i)
+                wv[u][i] = load_codes(a.w + (int64_t)min(n0 + 16 * i + (lane & 15), a.N - 1) * a.ldw, k, a.K);
 #pragma unroll
             for (int j = 0; j < TB; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, qv[j], acc[i][j], 0, 0, 0);
+                qv[u][j] = load_codes(a.q + (int64_t)min(t0 + 16 * j + (lane & 15), a.T - 1) * a.ldq, k, a.K);
         }
+        multiply();
     }
+    v4i *part = reinterpret_cast<v4i *>(slot);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < TB; ++j)
-            part[wave][i * TB + j][lane] = acc[i][j];
+            part[(i * TB + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     for (int f = threadIdx.x; f < RT * TB * 64; f += 64 * W) {
         const int l = f & 63, ij = f >> 6;
-        v4i sum = part[0][ij][l];
+        v4i sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 1; w < W; ++w)
-            sum += part[w][ij][l];
-        const int n = n0 + 16 * (ij / TB) + 4 * (l >> 4), t = t0 + 16 * (ij % TB) + (l & 15);
-        if (t < a.T) {
+        for (int w = 0; w < W; ++w)
+            sum += reinterpret_cast<const v4i *>(lds + w * ST)[f];
+        const int n = n0 + 16 * (ij / TB) + 4 * (l >> 4), c = 16 * (ij % TB) + (l & 15), t = t0 + c;
+        if (c < 8 * TC && t < a.T) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (n + i < a.N)
@@ -158,26 +206,30 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
 // there); needs rows of 16-byte alignment.  Otherwise they pass through
 // registers.  The last, partial stage always does (load_codes gives its zeros).
 // ---------------------------------------------------------------------------
-template <typename OT, bool DMA, int WT, int WN, int FT, int FN>
+template <typename OT, bool DMA, int NB, int WT, int WN, int FT, int FN>
 __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, int tiles_t, int tiles_n)
 {
-    constexpr int NW = WT * WN, NT = 64 * NW, BT = 32 * WT * FT, BN = 32 * WN * FN;
+    constexpr int NW = WT * WN, BT = 32 * WT * FT, BN = 32 * WN * FN;
     constexpr int CP = (BT + BN) / 8 / NW;               // 8-row copies per wave and stage
+    constexpr int BUF = (BT + BN) * 128;                 // bytes of a stage
     constexpr int TP = BT / 8 / NW;                      // of these, token rows
     static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole copies per wave");
-    // two buffers as two objects: the compiler then knows that reads of one do
-    // not wait for copies into the other
-    __shared__ __align__(128) uint8_t buf0[(BT + BN) * 128];
-    __shared__ __align__(128) uint8_t buf1[(BT + BN) * 128];
+    // the buffers are objects of their own: the compiler then knows that reads
+    // of one do not wait for copies into another
+    static_assert(NB >= 2 && NB <= 4, "two to four buffers");
+    __shared__ __align__(128) uint8_t buf0[BUF];
+    __shared__ __align__(128) uint8_t buf1[BUF];
+    __shared__ __align__(128) uint8_t buf2[NB > 2 ? BUF : 16];
+    __shared__ __align__(128) uint8_t buf3[NB > 3 ? BUF : 16];
 
     // tiles in groups of 8 token tiles, token tile fastest, each XCD (blocks
     // with the same index mod 8) a contiguous run of them
     const int per = gridDim.x >> 3, logical = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (logical >= tiles_t * tiles_n)
         return;
-    const int group = logical / (8 * tiles_n), in = logical - group * 8 * tiles_n;
-    const int gt = min(8, tiles_t - 8 * group);
-    const int t0 = (8 * group + in % gt) * BT, n0 = (in / gt) * BN;
+    const int band = logical / (8 * tiles_n), in = logical - band * 8 * tiles_n;
+    const int gt = min(8, tiles_t - 8 * band);
+    const int t0 = (8 * band + in % gt) * BT, n0 = (in / gt) * BN;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -221,8 +273,11 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
             for (int j = 0; j < FN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bv[set][j], av[set][i], acc[i][j], 0, 0, 0);
     };
-    v4i reg[DMA ? 1 : CP];
-    auto fetch = [&](uint8_t *buf, int ahead) {          // sets out a whole stage
+    // rows in registers on their way into LDS: two stages where there is room
+    constexpr int RD = DMA ? 0 : (FT * FN <= 4) ? 2 : 1;
+    static_assert(DMA || NB == 2, "through registers two buffers do");
+    v4i reg[RD ? RD : 1][DMA ? 1 : CP];
+    auto fetch = [&](uint8_t *buf, int set) {            // sets out the next whole stage
 #pragma unroll
         for (int i = 0; i < CP; ++i) {
             if constexpr (DMA)
@@ -230,24 +285,34 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
                     (const __attribute__((address_space(1))) void *)src[i],
                     (__attribute__((address_space(3))) void *)(buf + lds_at(i)), 16, 0, 0);
             else
-                reg[i] = load16(src[i]);
-            src[i] += ahead;
+                reg[set][i] = load16(src[i]);
+            src[i] += 128;
         }
     };
-    auto land = [&](uint8_t *buf) {
-        if constexpr (!DMA) {
+    auto land = [&](uint8_t *buf, int set) {
 #pragma unroll
-            for (int i = 0; i < CP; ++i)
-                *reinterpret_cast<v4i *>(buf + lds_at(i) + 16 * lane) = reg[i];
-        }
+        for (int i = 0; i < CP; ++i)
+            *reinterpret_cast<v4i *>(buf + lds_at(i) + 16 * lane) = reg[set][i];
     };
-    // the copies of this wave have landed, its reads are done; then every wave's
-    auto meet = [&]() {
+    // this wave's copies have landed but for those of the LEFT stages set out
+    // last, and its reads are done; then every wave's
+    auto meet = [&](auto left_) {
+        constexpr int LEFT = decltype(left_)::value * CP;
+        static_assert(LEFT < 64, "vmcnt counts to 63");
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);              // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);   // vmcnt(LEFT) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+    // the same where nothing is copied: loads into registers stay on their way
+    auto meet_lds = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xc07f);              // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    const std::integral_constant<int, 0> all;
+    const std::integral_constant<int, NB - 2> ahead;
     // within a K step: a fragment's read, a product, in turn, so that every read
     // is out before the last products and back before the next step's first
     auto interleave = [&]() {
@@ -258,13 +323,15 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    // Stage st in four K steps.  Step 0's fragments are in set 0 on entry.
-    // Before the last step is multiplied all of this stage has been read, so
-    // the waves meet there: from then on the next stage can be read and the
-    // one after it copied over this one.  Past the last stage the last one is
-    // fetched again and not used, so that all stages are the same code.
+    // Stage st in four K steps, from buffer cur; step 0's fragments are in set 0
+    // on entry.  Before the last step is multiplied all of this stage has been
+    // read, so the waves meet there: from then on the next stage can be read
+    // and the NB-th from here copied over this one.  The stages' end (MORE =
+    // false) waits for all copies and sets out none past the last.
     const int stages = a.K >> 7;
-    auto stage = [&](int st, uint8_t *cur, uint8_t *other) {
+    constexpr int LEAD = DMA ? NB : 1 + RD;              // the stage that stage st sets out: st + LEAD
+    auto stage = [&](auto more_, int st, uint8_t *cur, uint8_t *next, int set) {
+        constexpr bool MORE = decltype(more_)::value;
         read(1, cur, 1);
         multiply(0);
         interleave();
@@ -272,36 +339,80 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
         multiply(1);
         interleave();
         read(1, cur, 3);
-        land(other);
+        if constexpr (!DMA)
+            land(next, set);
         multiply(0);
         interleave();
-        meet();
-        read(0, other, 0);
-        fetch(cur, st + 3 < stages ? 128 : 0);
+        if constexpr (!DMA) {
+            meet_lds();
+        } else if constexpr (MORE) {
+            meet(ahead);
+        } else {
+            if (st + NB - 1 < stages)
+                meet(ahead);
+            else
+                meet(all);
+        }
+        read(0, next, 0);
+        if (MORE || st + LEAD < stages)
+            fetch(cur, set);
         multiply(1);
         interleave();
     };
     if (stages > 0) {
-        fetch(buf0, stages > 1 ? 128 : 0);
-        land(buf0);
-        meet();
-        fetch(buf1, stages > 2 ? 128 : 0);
-        read(0, buf0, 0);
-        int st = 0;
-        for (; st + 1 < stages; st += 2) {
-            stage(st, buf0, buf1);
-            stage(st + 1, buf1, buf0);
+        fetch(buf0, 0);
+        if constexpr (DMA) {
+            if (1 < stages)
+                fetch(buf1, 0);
+            if constexpr (NB > 2)
+                if (2 < stages)
+                    fetch(buf2, 0);
+            if constexpr (NB > 3)
+                if (3 < stages)
+                    fetch(buf3, 0);
+            if (stages >= NB)
+                meet(std::integral_constant<int, NB - 1>());
+            else
+                meet(all);
+        } else {
+            land(buf0, 0);
+            if (1 < stages)
+                fetch(buf1, RD - 1);
+            if (RD > 1 && 2 < stages)
+                fetch(buf0, 0);
+            meet_lds();
         }
-        if (stages & 1)
-            stage(st, buf0, buf1);
-        meet();                                          // no copy outlives the loop
+        read(0, buf0, 0);
+        constexpr std::true_type more{};
+        constexpr std::false_type end{};
+        constexpr int S1 = RD > 1 ? 1 : 0;               // register set of odd stages
+        int st = 0;
+        for (; st + NB - 1 + LEAD < stages; st += NB) {
+            stage(more, st, buf0, buf1, S1);
+            stage(more, st, buf1, NB > 2 ? buf2 : buf0, 0);
+            if constexpr (NB > 2)
+                stage(more, st, buf2, NB > 3 ? buf3 : buf0, 0);
+            if constexpr (NB > 3)
+                stage(more, st, buf3, buf0, 0);
+        }
+        for (; st < stages; st += NB) {
+            stage(end, st, buf0, buf1, S1);
+            if (st + 1 < stages)
+                stage(end, st + 1, buf1, NB > 2 ? buf2 : buf0, 0);
+            if constexpr (NB > 2)
+                if (st + 2 < stages)
+                    stage(end, st + 2, buf2, NB > 3 ? buf3 : buf0, 0);
+            if constexpr (NB > 3)
+                if (st + 3 < stages)
+                    stage(end, st + 3, buf3, buf0, 0);
+        }
     }
-    if (a.K & 127) {
-        // src points at the last whole stage, or at the row's start
-        const int k = (stages << 7) + 16 * piece, at = (max(stages - 1, 0) << 7) + 16 * piece;
+    const bool tail = (a.K & 127) != 0;
+    if (tail) {
+        const int k = 128 * stages + 16 * piece;         // src has come this far
 #pragma unroll
         for (int i = 0; i < CP; ++i) {
-            *reinterpret_cast<v4i *>(buf0 + lds_at(i) + 16 * lane) = load_codes(src[i] - at, k, a.K);
+            *reinterpret_cast<v4i *>(buf0 + lds_at(i) + 16 * lane) = load_codes(src[i] - k, k, a.K);
             asm volatile("" ::: "memory");               // one at a time: it is a single stage
         }
         __syncthreads();
@@ -321,9 +432,9 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     constexpr int PITCH = 32 * FN * (int)sizeof(OT) + 16;
     constexpr int LPR = 2 * FN * (int)sizeof(OT);        // lanes (16 bytes each) per row
     constexpr int VE = 16 / (int)sizeof(OT);             // values per lane
-    static_assert(32 * PITCH * NW / 2 <= (BT + BN) * 128, "half of the waves' parts fit one buffer");
+    static_assert(32 * PITCH * NW / 2 <= BUF, "half of the waves' parts fit one buffer");
     const int nw0 = n0 + 32 * FN * wn, tw0 = t0 + 32 * FT * wt;
-    if (a.K & 127)
+    if (tail)
         __syncthreads();                                 // buf0 has been read
     uint8_t *mine = (wave < NW / 2 ? buf0 : buf1) + (wave % (NW / 2)) * 32 * PITCH;
     float ws[FN][16], bias[FN][16];
@@ -358,9 +469,7 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
                 else
                     *reinterpret_cast<float4 *>(p) = make_float4(y[0], y[1], y[2], y[3]);
             }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_lds_sync();
 #pragma unroll
         for (int h = 0; h < LPR / 2; ++h) {              // 64/LPR rows each
             const int row = h * (64 / LPR) + lane / LPR, col = (lane % LPR) * VE;
@@ -379,39 +488,117 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
                 }
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_lds_sync();
     }
 }
 
-template <typename OT, int RT, int TB, int W, int U>
+template <typename OT, bool NT, int RT, int TC, int W>
 static void launch_stream(const LinArgs &a, hipStream_t st)
 {
-    const dim3 grid((a.N + 16 * RT - 1) / (16 * RT), (a.T + 16 * TB - 1) / (16 * TB));
-    launch(linear_stream_kernel<OT, RT, TB, W, U>, grid, 64 * W, 0, st, a);
+    const dim3 grid((a.N + 16 * RT - 1) / (16 * RT), (a.T + 8 * TC - 1) / (8 * TC));
+    launch(linear_stream_kernel<OT, NT, RT, TC, W>, grid, 64 * W, 0, st, a);
 }
 
-template <typename OT, bool DMA, int WT, int WN, int FT, int FN>
+template <typename OT, bool DMA, int NB, int WT, int WN, int FT, int FN>
 static void launch_tiles(const LinArgs &a, hipStream_t st)
 {
     const int tt = (a.T + 32 * WT * FT - 1) / (32 * WT * FT), tn = (a.N + 32 * WN * FN - 1) / (32 * WN * FN);
     const unsigned grid = ((unsigned)tt * tn + 7) / 8 * 8;
-    launch(linear_tiles_kernel<OT, DMA, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
+    launch(linear_tiles_kernel<OT, DMA, NB, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
+}
+
+// ---------------------------------------------------------------------------
+// Choice of a kernel.  Times in us on an MI355X, launches in a row.
+//
+// Stream: up to 64 tokens, and more where 32-channel x 64-token blocks still
+// find a CU each (256 x 2048 x 7168: 11.3, tiles 14.1; with one and a half
+// blocks per CU, 128 x 6144 x 6144, tiles win, 13.1 to 17.7).
+//  - Weight rows per block: 32; 16 where there are few channels (20 x 2048 x
+//    7168: 6.2 against 7.3) or at most 8 tokens (4 x 24576 x 6144: 22.8 against
+//    23.4); 48 with four waves from 24576 channels on, two blocks per CU, where
+//    the tokens are read less often (24 x 24576 x 6144: 26.7 against 28.1).
+//  - The non-temporal hint from 128 MiB of weights on, of which the 256 MiB
+//    last-level cache would not keep two (1 x 24576 x 6144: 23.2 with, 26.2
+//    without; 24: 26.7, 29.8).  Smaller weights may stay there from one call
+//    to the next and are read plainly: 32 x 6144 x 6144 8.9 from the cache, 12.1
+//    from memory; with the hint 11.7 from either.
+//
+// Tiles: a block's time is about its stages of 128 codes, each bound by what a
+// CU takes in (72 GB/s here, and 64 x 64 .. 128 x 256 tiles need 16 .. 48 KiB a
+// stage) or by its products (256 x 256), and a fixed part, the first stage's
+// way and the output.  Blocks go to 256 CUs; the tile with the smallest (blocks
+// per CU, rounded up) x (block's time) is taken.  Measured, 64x64 / 64x128 /
+// 128x128 / 128x256 / 256x256, K = 6144: 128 x 6144 13.1 / 18.6 / 25.2 / 36.9 / -;
+// 256 x 6144 21.5 / 19.1 / 25.3 / 37.0 / -; 512 x 6144 31.9 / 30.3 / 27.1 / 37.6 / -;
+// 1024 x 6144 63 / 51 / 55 / 42.8 / 65; 4096 x 24576 - / - / 664 / - / 535.
+// Rows that are not 16-byte aligned pass through registers and cross a line
+// each, which costs all tiles alike (4096 x 24576 x 6144: 770; 561 where the
+// rows are aligned).
+// ---------------------------------------------------------------------------
+template <typename OT, int TC>
+static void enqueue_stream(const LinArgs &a, hipStream_t st)
+{
+    const bool nt = (int64_t)a.N * a.K > (128 << 20);
+    if constexpr (TC == 1) {
+        nt ? launch_stream<OT, true, 1, TC, 8>(a, st) : launch_stream<OT, false, 1, TC, 8>(a, st);
+    } else {
+        if (nt && a.N >= 24576)
+            launch_stream<OT, true, 3, TC, 4>(a, st);
+        else if (nt)
+            launch_stream<OT, true, 2, TC, 8>(a, st);
+        else if (a.N > 4096 || a.T > 64)
+            launch_stream<OT, false, 2, TC, 8>(a, st);
+        else
+            launch_stream<OT, false, 1, TC, 8>(a, st);
+    }
+}
+
+template <typename OT, bool DMA>
+static void enqueue_tiles(const LinArgs &a, hipStream_t st)
+{
+    struct Tile {
+        int bt, bn;
+        double stage, fixed;                             // us of a block
+    };
+    static constexpr Tile tile[5] = {{64, 64, 0.21, 1.0},   {64, 128, 0.36, 1.5}, {128, 128, 0.52, 4.0},
+                                     {128, 256, 0.82, 4.0}, {256, 256, 1.55, 8.0}};
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < 5; ++i) {
+        const Tile &t = tile[i];
+        const int64_t blocks = (int64_t)((a.T + t.bt - 1) / t.bt) * ((a.N + t.bn - 1) / t.bn);
+        const double us = (double)((blocks + 255) / 256) * (t.stage * a.K / 128 + t.fixed);
+        if (i == 0 || us < least) {
+            best = i;
+            least = us;
+        }
+    }
+    // through registers two buffers do; copies go three or four stages ahead
+    // where the LDS has room
+    switch (best) {
+    case 0: launch_tiles<OT, DMA, DMA ? 4 : 2, 2, 2, 1, 1>(a, st); break;
+    case 1: launch_tiles<OT, DMA, DMA ? 3 : 2, 2, 2, 1, 2>(a, st); break;
+    case 2: launch_tiles<OT, DMA, DMA ? 3 : 2, 2, 2, 2, 2>(a, st); break;
+    case 3: launch_tiles<OT, DMA, DMA ? 3 : 2, 2, 4, 2, 2>(a, st); break;
+    default: launch_tiles<OT, DMA, 2, 2, 4, 4, 2>(a, st); break;
+    }
 }
 
 template <typename OT>
 static void enqueue_linear(const LinArgs &a, hipStream_t st)
 {
-    const bool dma = ops_aligned(a.q, 16) && ops_aligned(a.w, 16) && a.ldq % 16 == 0 && a.ldw % 16 == 0;
-    if (a.T <= 16)
-        launch_stream<OT, 1, 1, 8, 6>(a, st);
-    else if (a.T <= 64)
-        launch_stream<OT, 2, 2, 8, 4>(a, st);
-    else if (dma)
-        launch_tiles<OT, true, 2, 4, 4, 2>(a, st);
+    if (a.T <= 8)
+        enqueue_stream<OT, 1>(a, st);
+    else if (a.T <= 16)
+        enqueue_stream<OT, 2>(a, st);
+    else if (a.T <= 32)
+        enqueue_stream<OT, 4>(a, st);
+    else if (a.T <= 64 || (int64_t)((a.T + 63) / 64) * ((a.N + 31) / 32) <= 256)
+        enqueue_stream<OT, 8>(a, st);
+    else if (ops_aligned(a.q, 16) && ops_aligned(a.w, 16) && a.ldq % 16 == 0 && a.ldw % 16 == 0)
+        enqueue_tiles<OT, true>(a, st);
     else
-        launch_tiles<OT, false, 2, 4, 4, 2>(a, st);
+        enqueue_tiles<OT, false>(a, st);
 }
 
 }  // namespace moe

@@ -41,8 +41,9 @@ def check_codes(q, s, v, tol):
 
 
 def linear(q, s, w, ws, bias):
-    """The definition, with its fp32 epilogue: bits are defined."""
-    acc = q.astype(np.int64) @ w.astype(np.int64).T
+    """The definition, with its fp32 epilogue: bits are defined.  (fp64 products
+    and sums of codes are whole numbers far below 2^53: exact.)"""
+    acc = q.astype(np.float64) @ w.astype(np.float64).T
     assert np.abs(acc).max(initial=0) < 2 ** 31
     y = acc.astype(np.float32) * s.astype(np.float32)[:, None] * ws.astype(np.float32)
     return y if bias is None else y + bias.astype(np.float32)

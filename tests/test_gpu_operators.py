@@ -275,6 +275,24 @@ def test_linear_many_tokens(T, N, K):
     check_linear(run_linear(q, s, w, ws, None, "f32"), q, s, w, ws, None, "f32")
 
 
+@pytest.mark.parametrize("T,N,K", [(200, 5003, 384), (1999, 2001, 1040), (2047, 4090, 640), (4001, 4093, 520)])
+@pytest.mark.parametrize("pad", [0, 16, 3])
+def test_linear_every_tile_and_alignment(T, N, K, pad):
+    # shapes that spread over the chip as 64 x 128, 128 x 128, 128 x 256 and
+    # 256 x 256 tiles, whole and partial stages, aligned rows and others
+    q, s, w, ws, b = lin_inputs(6, T, N, K)
+    check_linear(run_linear(q, s, w, ws, b, "bf16", pad), q, s, w, ws, b, "bf16")
+    check_linear(run_linear(q, s, w, ws, None, "f32", pad), q, s, w, ws, None, "f32")
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 6200, 21700), (12, 24600, 5505), (24, 24577, 5504), (40, 6200, 21700)])
+def test_linear_weights_beyond_the_cache(T, N, K):
+    r = np.random.default_rng([7, T, N])
+    q, w = r.integers(-128, 128, (T, K), dtype=np.int8), r.integers(-128, 128, (N, K), dtype=np.int8)
+    s, ws = (0.01 + r.random(T)).astype(np.float32), (0.01 + r.random(N)).astype(np.float32)
+    check_linear(run_linear(q, s, w, ws, None, "bf16"), q, s, w, ws, None, "bf16")
+
+
 @pytest.mark.parametrize("T", [1, 20, 300])
 def test_linear_longest_sum_does_not_overflow(T):
     K = 131071

@@ -153,10 +153,12 @@ def addr(x):
     """Device/host address of a tensor, numpy array, int or None."""
     if x is None:
         return None
+    try:
+        return x.data_ptr()                     # the common case, without asking first
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError("cannot take the address of %r" % type(x))

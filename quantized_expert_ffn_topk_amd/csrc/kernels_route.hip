@@ -41,20 +41,6 @@ __device__ __forceinline__ uint64_t order_key(double c)
     return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
-// Maximum over the wave, in every lane (a scalar): DPP row shifts and
-// broadcasts bring it to lane 63.  Lanes that a step does not reach take 0.
-__device__ __forceinline__ uint32_t wave_top(uint32_t v)
-{
-#define STEP(ctrl, rows) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
-    STEP(0x111, 0xf);              // row_shr:1
-    STEP(0x112, 0xf);
-    STEP(0x114, 0xf);
-    STEP(0x118, 0xf);
-    STEP(0x142, 0xa);              // row_bcast:15 into rows 1 and 3
-    STEP(0x143, 0xc);              // row_bcast:31 into rows 2 and 3
-#undef STEP
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
 __device__ __forceinline__ uint64_t wave_top(uint64_t v)
 {
     const uint32_t hi = wave_top((uint32_t)(v >> 32));
@@ -76,17 +62,11 @@ __device__ __forceinline__ double lane_value(double v, int l)
 
 __device__ __forceinline__ float wave_sum(float v)
 {
-    v += xor_lane_f<32>(v);
-    v += xor_lane_f<16>(v);
-    v += xor_lane_f<8>(v);
-    v += xor_lane_f<4>(v);
-    v += xor_lane_f<2>(v);
-    v += xor_lane_f<1>(v);
-    return v;
+    return wave_total_f(v);
 }
 __device__ __forceinline__ double wave_sum(double v)
 {
-    return wave_sum_d(v);
+    return wave_total_d(v);
 }
 __device__ __forceinline__ float exp_of(float v)
 {

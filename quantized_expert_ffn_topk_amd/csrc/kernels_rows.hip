@@ -17,6 +17,7 @@ struct NormArgs {
     const float *gamma;        // NULL: ones
     RT *h;                     // NULL: not wanted
     int64_t ldx, ldr, ldh;
+    double inv_n;              // 1/n
     float eps;
 };
 template <typename XT>
@@ -50,18 +51,17 @@ __device__ __forceinline__ float silu_mul(float g, float u)
 }
 
 // ---------------------------------------------------------------------------
-// One row by NT threads, NV vectors of 8 values per thread (8*NT*NV >= n), the
-// row in registers between its one read and its writes.  A thread's vector i
-// covers values [col, col+8), col = 8*(lane + NT*i); one that passes the row's
-// end reads (and writes again, with the same values) the row's last 8 values,
-// of which `first` counts those that are not its own in the sum.  Rows shorter
-// than 8 are read value by value.
+// One row by NT threads, NV vectors of 8 values per thread (8*NT*NV >= n >= 8),
+// the row in registers between its one read and its writes.  A thread's vector
+// i covers values [col, col+8), col = 8*(lane + NT*i).  One that passes the
+// row's end reads the row's last 8 values instead (c < col), counts those of
+// its own in the sum and writes all of them again, with the same values.
 // NT = 64: a wave per row, four rows per block, no barrier.
 // ---------------------------------------------------------------------------
 template <int NT>
 __device__ __forceinline__ double row_sum_d(double v, double *red)
 {
-    v = wave_sum_d(v);
+    v = wave_total_d(v);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0)
             red[threadIdx.x >> 6] = v;
@@ -77,7 +77,7 @@ __device__ __forceinline__ double row_sum_d(double v, double *red)
 template <int NT>
 __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, uint32_t *red)
 {
-    v = wave_max_u32(v);
+    v = wave_top(v);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0)
             red[threadIdx.x >> 6] = v;
@@ -90,9 +90,23 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, uint32_t *red)
     return v;
 }
 
-// scale and multiplier of a row whose largest magnitude has the fp32 bits m.
-// Rows below 2^-96 are multiplied by 2^64 first (exact), so that 127/max stays
-// finite.
+// fp32(1/sqrt(x)): the hardware's fp64 estimate and two Newton steps, far
+// within fp32's unit (the exact fp64 root and quotient took a fifth of the
+// norm's instructions); 0 for infinity, NaN for NaN
+__device__ __forceinline__ float inv_sqrt(double x)
+{
+    const double r0 = __builtin_amdgcn_rsq(x);
+    double r = r0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r = r * fma(-0.5 * x * r, r, 1.5);
+    return (float)((x < (double)INFINITY) ? r : r0);
+}
+
+// The scale of a row whose largest magnitude has the fp32 bits m, and the
+// multiplier of its codes: rows below 2^-96 are multiplied by pre = 2^64 first
+// (exact), so that 127/max stays finite.  inv = 0 for a row of zeros and for
+// one with a NaN or an infinity.
 __device__ __forceinline__ void row_scale(uint32_t m, float *s, float *pre, float *inv)
 {
     const float a = __uint_as_float(m);
@@ -101,46 +115,36 @@ __device__ __forceinline__ void row_scale(uint32_t m, float *s, float *pre, floa
     *inv = (m == 0u) ? 0.0f : 127.0f / (a * *pre);
     if (m >= 0x7f800000u) {
         *s = __uint_as_float(0x7fc00000u);
-        *pre = *inv = 0.0f;
+        *inv = 0.0f;
     }
 }
 
-// rint(v*pre*inv) clamped, as the low byte; 0 throughout where inv is 0 (a row
-// of zeros, or one with a NaN or an infinity, whose products may be NaN)
-__device__ __forceinline__ uint32_t code(float v, float pre, float inv)
+// rint of |p| <= 127.5 in the low byte: adding 1.5*2^23 rounds to the nearest
+// whole number, ties to even
+__device__ __forceinline__ uint32_t code(float p)
 {
-    const float r = fminf(fmaxf(rintf((v * pre) * inv), -127.0f), 127.0f);
-    return (inv == 0.0f) ? 0u : (uint32_t)(int)r & 0xffu;
+    return __float_as_uint(p + 12582912.0f);
+}
+// four codes in a word
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __builtin_amdgcn_perm(code(b), code(a), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code(d), code(c), 0x0c0c0400u);
+    return lo | hi << 16;
 }
 
-template <int NT, int NV, typename LoadFn, typename MidFn>
-__device__ __forceinline__ void row_body(const RowOut &o, int t, int lane, bool live,
-                                         uint32_t *red, LoadFn load, MidFn mid)
+// y_out, codes and scale of a row whose values are in v
+template <int NT, int NV>
+__device__ __forceinline__ void row_out(const RowOut &o, int t, int lane, bool live, uint32_t *red,
+                                        float (&v)[NV][8], const int (&c)[NV])
 {
     const int n = o.n;
-    float v[NV][8];
-    int c[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        c[i] = max(0, min(8 * (lane + NT * i), n - 8));
-    load(v, c);
-    mid(v, c);
-    const bool tiny = n < 8;
     if (o.y && live) {
         bf16_t *yr = o.y + (int64_t)t * o.ldy;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (8 * (lane + NT * i) >= n)
-                continue;
-            if (!tiny) {
+        for (int i = 0; i < NV; ++i)
+            if (8 * (lane + NT * i) < n)
                 store8(yr + c[i], v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n)
-                        store1(yr + j, v[i][j]);
-            }
-        }
     }
     if (!o.q)
         return;
@@ -155,160 +159,164 @@ __device__ __forceinline__ void row_body(const RowOut &o, int t, int lane, bool 
     row_scale(m, &s, &pre, &inv);
     if (!live)
         return;
+    if (pre != 1.0f) {                              // the whole row alike
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] *= pre;
+    }
     int8_t *qr = o.q + (int64_t)t * o.ldq;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (8 * (lane + NT * i) >= n)
-            continue;
-        uint32_t d[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            d[j] = code(v[i][j], pre, inv);
-        if (!tiny) {
-            bytes8_a1 b;
-            b.d[0] = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
-            b.d[1] = d[4] | d[5] << 8 | d[6] << 16 | d[7] << 24;
+        const float *p = v[i];
+        bytes8_a1 b;
+        b.d[0] = code4(p[0] * inv, p[1] * inv, p[2] * inv, p[3] * inv);
+        b.d[1] = code4(p[4] * inv, p[5] * inv, p[6] * inv, p[7] * inv);
+        if (inv == 0.0f)
+            b.d[0] = b.d[1] = 0u;
+        if (8 * (lane + NT * i) < n)
             *reinterpret_cast<bytes8_a1 *>(qr + c[i]) = b;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n)
-                    qr[j] = (int8_t)d[j];
-        }
     }
     if (lane == 0)
         o.s[t] = s;
 }
 
-// 8 values at column c of a row of n (value by value where n < 8, zeros past n)
-template <typename XT>
-__device__ __forceinline__ void row_load8(const XT *p, int c, int n, float (&v)[8])
-{
-    if (n >= 8) {
-        load8(p + c, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = (j < n) ? to_f32(p[j]) : 0.0f;
-    }
-}
-
-template <int NT>
-constexpr int rows_per_block()
-{
-    return NT == 64 ? 4 : 1;
-}
 template <int NT>
 constexpr int block_threads()
 {
     return NT == 64 ? 256 : NT;
 }
 
-template <int NT, int NV, typename XT, typename RT>
+// Row and lane of a thread; a wave past the rows (NT = 64) repeats the last
+// row and stores nothing.
+template <int NT>
+__device__ __forceinline__ bool row_of(int T, int *t, int *lane)
+{
+    const int row = (NT == 64) ? (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6) : (int)blockIdx.x;
+    *lane = (NT == 64) ? threadIdx.x & 63 : threadIdx.x;
+    *t = min(row, T - 1);
+    return row < T;
+}
+
+// RES: there is a residual.  All loads of the row and of gamma are issued
+// before any value is used.
+template <int NT, int NV, typename XT, typename RT, bool RES>
 __global__ __launch_bounds__(block_threads<NT>()) void rmsnorm_kernel(NormArgs<XT, RT> a, RowOut o)
 {
     __shared__ double red_d[NT / 64];
     __shared__ uint32_t red_m[NT / 64];
-    const int lane = (NT == 64) ? threadIdx.x & 63 : threadIdx.x;
-    const int row = (NT == 64) ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-    const bool live = row < o.T;
-    const int t = live ? row : o.T - 1;            // a wave past the rows repeats the last, stores nothing
+    int t, lane;
+    const bool live = row_of<NT>(o.T, &t, &lane);
     const int n = o.n;
-    row_body<NT, NV>(
-        o, t, lane, live, red_m,
-        [&](float (&v)[NV][8], const int (&c)[NV]) {
-            const XT *xr = a.x + (int64_t)t * a.ldx;
+    int c[NV];
+    float v[NV][8], g[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        c[i] = min(8 * (lane + NT * i), n - 8);
+    {
+        raw8<XT> x[NV];
+        raw8<RT> r[RES ? NV : 1];
+        const XT *xr = a.x + (int64_t)t * a.ldx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            x[i].load(xr + c[i]);
+        if constexpr (RES) {
+            const RT *rr = a.res + (int64_t)t * a.ldr;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                row_load8(xr, c[i], n, v[i]);
-            if (a.res) {
-                const RT *rr = a.res + (int64_t)t * a.ldr;
-                float r[NV][8];
+                r[i].load(rr + c[i]);
+        }
+        if (a.gamma) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    row_load8(rr, c[i], n, r[i]);
+            for (int i = 0; i < NV; ++i)
+                load8(a.gamma + c[i], g[i]);
+        } else {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[i][j] += r[i][j];
+                for (int j = 0; j < 8; ++j)
+                    g[i][j] = 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i].widen(v[i]);
+            if constexpr (RES) {
+                float w[8];
+                r[i].widen(w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] += w[j];
             }
-        },
-        [&](float (&v)[NV][8], const int (&c)[NV]) {
-            double ss = 0.0;
+        }
+    }
+    double ss = 0.0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int col = 8 * (lane + NT * i);
+    for (int i = 0; i < NV; ++i) {
+        const int col = 8 * (lane + NT * i);
+        if (col + 8 <= n) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const double d = (c[i] + j >= col) ? (double)v[i][j] : 0.0;
-                    ss = fma(d, d, ss);
-                }
+            for (int j = 0; j < 8; ++j)
+                ss = fma((double)v[i][j], (double)v[i][j], ss);
+        } else if (col < n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const double d = (c[i] + j >= col) ? (double)v[i][j] : 0.0;
+                ss = fma(d, d, ss);
             }
-            ss = row_sum_d<NT>(ss, red_d);
-            const float r = (float)(1.0 / sqrt(ss / (double)n + (double)a.eps));
-            if (a.h && live) {
-                RT *hr = a.h + (int64_t)t * a.ldh;
+        }
+    }
+    ss = row_sum_d<NT>(ss, red_d);
+    const float r = inv_sqrt(ss * a.inv_n + (double)a.eps);
+    if (a.h && live) {
+        RT *hr = a.h + (int64_t)t * a.ldh;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if (8 * (lane + NT * i) >= n)
-                        continue;
-                    if (n >= 8) {
-                        store8(hr + c[i], v[i]);
-                    } else {
+        for (int i = 0; i < NV; ++i)
+            if (8 * (lane + NT * i) < n)
+                store8(hr + c[i], v[i]);
+    }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j < n)
-                                store1(hr + j, v[i][j]);
-                    }
-                }
-            }
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float g[8];
-                if (a.gamma)
-                    row_load8(a.gamma, c[i], n, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float y = v[i][j] * r;
-                    v[i][j] = a.gamma ? y * g[j] : y;
-                }
-            }
-        });
+        for (int j = 0; j < 8; ++j)
+            v[i][j] = v[i][j] * r * g[i][j];
+    row_out<NT, NV>(o, t, lane, live, red_m, v, c);
 }
 
 template <int NT, int NV, typename XT>
 __global__ __launch_bounds__(block_threads<NT>()) void swiglu_kernel(SwigluArgs<XT> a, RowOut o)
 {
     __shared__ uint32_t red_m[NT / 64];
-    const int lane = (NT == 64) ? threadIdx.x & 63 : threadIdx.x;
-    const int row = (NT == 64) ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-    const bool live = row < o.T;
-    const int t = live ? row : o.T - 1;
+    int t, lane;
+    const bool live = row_of<NT>(o.T, &t, &lane);
     const int n = o.n;
-    row_body<NT, NV>(
-        o, t, lane, live, red_m,
-        [&](float (&v)[NV][8], const int (&c)[NV]) {
-            const XT *gr = a.gu + (int64_t)t * a.ld;
-            const XT *ur = gr + n;
-            float u[NV][8];
+    int c[NV];
+    float v[NV][8];
+    const XT *gr = a.gu + (int64_t)t * a.ld, *ur = gr + n;
+    raw8<XT> g[NV], u[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                row_load8(gr, c[i], n, v[i]);
-                row_load8(ur, c[i], n, u[i]);
-            }
+    for (int i = 0; i < NV; ++i)
+        c[i] = min(8 * (lane + NT * i), n - 8);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        g[i].load(gr + c[i]);
+        u[i].load(ur + c[i]);
+    }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[i][j] = silu_mul(v[i][j], u[i][j]);
-        },
-        [&](float (&)[NV][8], const int (&)[NV]) {});
+    for (int i = 0; i < NV; ++i) {
+        float w[8];
+        g[i].widen(v[i]);
+        u[i].widen(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[i][j] = silu_mul(v[i][j], w[j]);
+    }
+    row_out<NT, NV>(o, t, lane, live, red_m, v, c);
 }
 
 // ---------------------------------------------------------------------------
-// Rows too long for the registers (n > 32768): 1024 threads read the row again
-// for each step; every value is read and written by one thread, the writes in
+// Rows too long for the registers (n > 32768), or shorter than a vector (n < 8):
+// value by value, a block reads the row again for each step; every value is read and written by one thread, the writes in
 // the last step, so h_out may be an input here too.
 // ---------------------------------------------------------------------------
 template <typename XT, typename RT>
@@ -329,7 +337,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs<XT, RT> a, 
         ss = fma(d, d, ss);
     }
     ss = row_sum_d<1024>(ss, red_d);
-    const float r = (float)(1.0 / sqrt(ss / (double)n + (double)a.eps));
+    const float r = inv_sqrt(ss * a.inv_n + (double)a.eps);
     auto normed = [&](float h, int i) {
         const float y = h * r;
         return a.gamma ? y * a.gamma[i] : y;
@@ -349,7 +357,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs<XT, RT> a, 
         if (o.y)
             store1(o.y + (int64_t)t * o.ldy + i, v);
         if (o.q)
-            o.q[(int64_t)t * o.ldq + i] = (int8_t)code(v, pre, inv);
+            o.q[(int64_t)t * o.ldq + i] = (inv == 0.0f) ? 0 : (int8_t)(code((v * pre) * inv) & 0xffu);
     }
     if (o.q && threadIdx.x == 0)
         o.s[t] = s;
@@ -374,67 +382,81 @@ __global__ __launch_bounds__(1024) void swiglu_long_kernel(SwigluArgs<XT> a, Row
         if (o.y)
             store1(o.y + (int64_t)t * o.ldy + i, v);
         if (o.q)
-            o.q[(int64_t)t * o.ldq + i] = (int8_t)code(v, pre, inv);
+            o.q[(int64_t)t * o.ldq + i] = (inv == 0.0f) ? 0 : (int8_t)(code((v * pre) * inv) & 0xffu);
     }
     if (o.q && threadIdx.x == 0)
         o.s[t] = s;
 }
 
 // ---------------------------------------------------------------------------
-// Shapes: the fewest threads that hold the row in at most 4 vectors each.
+// Shapes.  Many rows: few vectors are left idle and a block is small.  Few rows
+// (fewer than the 256 CUs): as many threads on a row as it has vectors, up to
+// 1024, since only the row's own latency counts.
 // ---------------------------------------------------------------------------
-template <int NT, typename F>
-static void with_nv(int n, F &&f)
-{
-    const int nv = (n + 8 * NT - 1) / (8 * NT);
-    if (nv <= 1)
-        f(std::integral_constant<int, 1>());
-    else if (nv == 2)
-        f(std::integral_constant<int, 2>());
-    else if (nv == 3)
-        f(std::integral_constant<int, 3>());
-    else
-        f(std::integral_constant<int, 4>());
-}
+constexpr int ROW_REG_MAX = 32768;
+
+template <int V>
+using num = std::integral_constant<int, V>;
 
 template <typename F>
-static void with_shape(int n, F &&f)
+static void with_shape(int n, int T, F &&f)
 {
-    if (n <= 64 * 32)
-        with_nv<64>(n, [&](auto nv) { f(std::integral_constant<int, 64>(), nv); });
-    else if (n <= 256 * 32)
-        with_nv<256>(n, [&](auto nv) { f(std::integral_constant<int, 256>(), nv); });
-    else
-        with_nv<1024>(n, [&](auto nv) { f(std::integral_constant<int, 1024>(), nv); });
+    if (T < 256) {
+        if (n <= 512)
+            return f(num<64>(), num<1>());
+        if (n <= 2048)
+            return f(num<256>(), num<1>());
+        if (n <= 8192)
+            return f(num<1024>(), num<1>());
+        if (n <= 16384)
+            return f(num<1024>(), num<2>());
+    }
+    if (n <= 512)
+        return f(num<64>(), num<1>());
+    if (n <= 1024)
+        return f(num<64>(), num<2>());
+    if (n <= 2048)
+        return f(num<64>(), num<4>());
+    if (n <= 4096)
+        return f(num<256>(), num<2>());
+    if (n <= 6144)
+        return f(num<256>(), num<3>());
+    if (n <= 8192)
+        return f(num<256>(), num<4>());
+    if (n <= 12288)
+        return f(num<512>(), num<3>());
+    if (n <= 16384)
+        return f(num<512>(), num<4>());
+    if (n <= 24576)
+        return f(num<1024>(), num<3>());
+    f(num<1024>(), num<4>());
 }
-
-constexpr int ROW_REG_MAX = 32768;
 
 static unsigned row_grid(int T, int nt)
 {
-    return nt == 64 ? (unsigned)(((int64_t)T + 3) / 4) : (unsigned)T;
+    return nt == 64 ? (unsigned)((T + 3) / 4) : (unsigned)T;
 }
 
-template <typename XT, typename RT>
+template <bool RES, typename XT, typename RT>
 static void enqueue_norm(const NormArgs<XT, RT> &a, const RowOut &o, hipStream_t st)
 {
-    if (o.n > ROW_REG_MAX) {
+    if (o.n > ROW_REG_MAX || o.n < 8) {
         launch(rmsnorm_long_kernel<XT, RT>, (unsigned)o.T, 1024, 0, st, a, o);
         return;
     }
-    with_shape(o.n, [&](auto nt, auto nv) {
-        launch(rmsnorm_kernel<nt(), nv(), XT, RT>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
+    with_shape(o.n, o.T, [&](auto nt, auto nv) {
+        launch(rmsnorm_kernel<nt(), nv(), XT, RT, RES>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
     });
 }
 
 template <typename XT>
 static void enqueue_swiglu(const SwigluArgs<XT> &a, const RowOut &o, hipStream_t st)
 {
-    if (o.n > ROW_REG_MAX) {
+    if (o.n > ROW_REG_MAX || o.n < 8) {
         launch(swiglu_long_kernel<XT>, (unsigned)o.T, 1024, 0, st, a, o);
         return;
     }
-    with_shape(o.n, [&](auto nt, auto nv) {
+    with_shape(o.n, o.T, [&](auto nt, auto nv) {
         launch(swiglu_kernel<nt(), nv(), XT>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
     });
 }
@@ -499,18 +521,23 @@ extern "C" moe_status moe_rmsnorm_quant(const void *x, int32_t x_dtype, int64_t 
         return st;
     const RowOut o{static_cast<bf16_t *>(y_out), q, s, ldy, ldq, T, H};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    auto with = [&](auto xt, auto rt) {
-        typedef decltype(xt) XT;
-        typedef decltype(rt) RT;
+    auto with = [&](auto res, auto xt, auto rt) {
+        typedef std::remove_const_t<decltype(xt)> XT;
+        typedef std::remove_const_t<decltype(rt)> RT;
         const NormArgs<XT, RT> a{static_cast<const XT *>(x), static_cast<const RT *>(residual), gamma,
-                                 static_cast<RT *>(h_out), ldx, ldr, ldh, eps};
-        enqueue_norm(a, o, hs);
+                                 static_cast<RT *>(h_out), ldx, ldr, ldh, 1.0 / (double)H, eps};
+        enqueue_norm<decltype(res)::value>(a, o, hs);
     };
-    const bool rf = (residual || h_out) ? res_dtype == MOE_DT_F32 : x_dtype == MOE_DT_F32;
-    if (x_dtype == MOE_DT_F32)
-        rf ? with(0.0f, 0.0f) : with(0.0f, bf16_t(0));
+    const std::true_type yes;
+    const std::false_type no;
+    const float f = 0.0f;
+    const bf16_t b = 0;
+    if (!residual)                                  // h_out then has x's dtype
+        x_dtype == MOE_DT_F32 ? with(no, f, f) : with(no, b, b);
+    else if (x_dtype == MOE_DT_F32)
+        res_dtype == MOE_DT_F32 ? with(yes, f, f) : with(yes, f, b);
     else
-        rf ? with(bf16_t(0), 0.0f) : with(bf16_t(0), bf16_t(0));
+        res_dtype == MOE_DT_F32 ? with(yes, b, f) : with(yes, b, b);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? MOE_OK : hip_fail(e, "norm launch");
 }

@@ -71,24 +71,47 @@ __device__ __forceinline__ float to_f32(bf16_t v)
     return bf16_to_f32(v);
 }
 
-__device__ __forceinline__ void load8(const bf16_t *p, float (&v)[8])
-{
-    const bytes16_a2 b = *reinterpret_cast<const bytes16_a2 *>(p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(b.d[j] << 16);
-        v[2 * j + 1] = __uint_as_float(b.d[j] & 0xffff0000u);
+// 8 values as they lie in memory: loaded now, widened to fp32 when used
+template <typename T>
+struct raw8;
+template <>
+struct raw8<bf16_t> {
+    bytes16_a2 b;
+    __device__ __forceinline__ void load(const bf16_t *p)
+    {
+        b = *reinterpret_cast<const bytes16_a2 *>(p);
     }
-}
+    __device__ __forceinline__ void widen(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(b.d[j] << 16);
+            v[2 * j + 1] = __uint_as_float(b.d[j] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct raw8<float> {
+    bytes16_a4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = *reinterpret_cast<const bytes16_a4 *>(p);
+        b = *reinterpret_cast<const bytes16_a4 *>(p + 4);
+    }
+    __device__ __forceinline__ void widen(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(a.d[j]);
+            v[4 + j] = __uint_as_float(b.d[j]);
+        }
+    }
+};
 __device__ __forceinline__ void load8(const float *p, float (&v)[8])
 {
-    const bytes16_a4 a = *reinterpret_cast<const bytes16_a4 *>(p);
-    const bytes16_a4 b = *reinterpret_cast<const bytes16_a4 *>(p + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[j] = __uint_as_float(a.d[j]);
-        v[4 + j] = __uint_as_float(b.d[j]);
-    }
+    raw8<float> r;
+    r.load(p);
+    r.widen(v);
 }
 
 // two fp32 -> two bf16 in one word, round to nearest even (v_cvt_pk_bf16_f32)
@@ -128,15 +151,57 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     *reinterpret_cast<bytes16_a4 *>(p + 4) = b;
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
+// ---------------------------------------------------------------------------
+// device: maximum and sum over a wave, in every lane.  DPP row shifts and
+// broadcasts bring them to lane 63 in six dependent VALU steps (the swizzles
+// of xor_lane go through the LDS unit, several times as long each).  Lanes
+// that a step does not reach take 0.
+// ---------------------------------------------------------------------------
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp0(int v)
 {
-    v = max(v, (uint32_t)xor_lane<32>((int)v));
-    v = max(v, (uint32_t)xor_lane<16>((int)v));
-    v = max(v, (uint32_t)xor_lane<8>((int)v));
-    v = max(v, (uint32_t)xor_lane<4>((int)v));
-    v = max(v, (uint32_t)xor_lane<2>((int)v));
-    v = max(v, (uint32_t)xor_lane<1>((int)v));
-    return v;
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+#define MOE_DPP_STEPS(STEP)                                                              \
+    STEP(0x111, 0xf)   /* row_shr:1 */                                                   \
+    STEP(0x112, 0xf)                                                                     \
+    STEP(0x114, 0xf)                                                                     \
+    STEP(0x118, 0xf)                                                                     \
+    STEP(0x142, 0xa)   /* row_bcast:15 into rows 1 and 3 */                              \
+    STEP(0x143, 0xc)   /* row_bcast:31 into rows 2 and 3 */
+
+__device__ __forceinline__ uint32_t wave_top(uint32_t v)
+{
+#define STEP(c, r) v = max(v, (uint32_t)dpp0<c, r>((int)v));
+    MOE_DPP_STEPS(STEP)
+#undef STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// fixed order of additions
+__device__ __forceinline__ double wave_total_d(double v)
+{
+#define STEP(c, r)                                                                       \
+    {                                                                                    \
+        const long long u = __double_as_longlong(v);                                     \
+        const uint32_t lo = (uint32_t)dpp0<c, r>((int)(u & 0xffffffffll));               \
+        const uint32_t hi = (uint32_t)dpp0<c, r>((int)(u >> 32));                        \
+        v += __longlong_as_double((long long)((uint64_t)hi << 32 | lo));                 \
+    }
+    MOE_DPP_STEPS(STEP)
+#undef STEP
+    const long long u = __double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(u & 0xffffffffll), 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+__device__ __forceinline__ float wave_total_f(float v)
+{
+#define STEP(c, r) v += __int_as_float(dpp0<c, r>(__float_as_int(v)));
+    MOE_DPP_STEPS(STEP)
+#undef STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 }  // namespace moe

@@ -43,14 +43,6 @@ __device__ __forceinline__ v4i load_codes(const int8_t *row, int k, int K)
     return v;
 }
 
-// LDS written by lanes of a wave and read by others of the same wave
-__device__ __forceinline__ void wave_lds_sync()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 template <typename OT>
 __device__ __forceinline__ void store_out(const LinArgs &a, int t, int n, int acc)
 {

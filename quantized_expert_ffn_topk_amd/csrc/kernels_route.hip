@@ -3,9 +3,14 @@
 // best experts inside them, weights renormalised or as they are.
 //
 // One wave per token, expert e on lane e/NE (register e%NE), so that the first
-// lane of a ballot holds the lowest expert.  A token's logits are read once
-// and everything up to the k results stays in registers (the group scores pass
-// through LDS); the time is the launch and the k dependent wave maxima.
+// lane of a ballot holds the lowest expert.  Each lane sorts its NE candidates
+// once; then k times the best of the 64 first candidates is taken (a DPP
+// maximum over the wave) and its lane moves on.  A token's logits are read once
+// and stay in registers.  Bound by instructions, the k dependent maxima first
+// among them: 16 tokens of 256 experts in 8 groups 3.9 us, 4096 5.75, 16384
+// 15.7 (launches in a graph; 4.2 MB in and out at 4096 would take 1 us).  With
+// the best found among all NE registers each time, the library's exp and IEEE
+// quotients, 4096 took 7.4.
 #include "ops_common.h"
 
 #include <cmath>
@@ -20,6 +25,8 @@ struct SelectArgs {
     int softmax, n_group, topk_group, group_best, renorm;
     float scale;
     uint32_t gs, gs_inv;           // experts per group, ceil(2^22 / gs)
+    int lanes;                     // lanes that hold a group's experts and no others, a power
+                                   // of two; 0: there is no such number
     int32_t *idx;
     float *w;
     double *part2;                 // fp64 logits in two parts: the second, added and kept
@@ -68,13 +75,120 @@ __device__ __forceinline__ double wave_sum(double v)
 {
     return wave_total_d(v);
 }
+// exp and reciprocal.  fp32: 2^(v*log2 e) with the product's remainder added, so
+// that the error does not grow with |v|, and the hardware's reciprocal, each
+// about a unit in the last place (the library's exp and an IEEE quotient were a
+// fifth of the selection's instructions); fp64: the library's.
 __device__ __forceinline__ float exp_of(float v)
 {
-    return expf(v);
+    const float L2E = 1.44269502f, L2E_LO = 1.92596303e-8f;   // log2(e) = L2E + L2E_LO
+    const float t = v * L2E;
+    const float r = fmaf(v, L2E, -t) + v * L2E_LO;
+    const float e = __builtin_amdgcn_exp2f(t);
+    // past 2^126 (and for -inf) 0 or infinity as it is
+    return (fabsf(t) < 126.0f) ? fmaf(e, r * 0.693147181f, e) : e;
 }
 __device__ __forceinline__ double exp_of(double v)
 {
     return exp(v);
+}
+__device__ __forceinline__ float inverse(float v)
+{
+    return __builtin_amdgcn_rcpf(v);
+}
+__device__ __forceinline__ double inverse(double v)
+{
+    return 1.0 / v;
+}
+
+// A candidate: its key and its expert, in the order of choice: the larger key,
+// of equal ones the lower expert.
+template <typename Key>
+struct Cand;
+template <>
+struct Cand<uint32_t> {
+    uint64_t v;
+    __device__ __forceinline__ void set(uint32_t key, int e)
+    {
+        v = (uint64_t)key << 32 | (uint32_t)~e;
+    }
+    __device__ __forceinline__ uint32_t key() const
+    {
+        return (uint32_t)(v >> 32);
+    }
+    __device__ __forceinline__ int expert() const
+    {
+        return (int)~(uint32_t)v;
+    }
+    __device__ __forceinline__ bool before(const Cand &o) const
+    {
+        return v > o.v;
+    }
+};
+template <>
+struct Cand<uint64_t> {
+    uint64_t k;
+    int e;
+    __device__ __forceinline__ void set(uint64_t key, int expert)
+    {
+        k = key;
+        e = expert;
+    }
+    __device__ __forceinline__ uint64_t key() const
+    {
+        return k;
+    }
+    __device__ __forceinline__ int expert() const
+    {
+        return e;
+    }
+    __device__ __forceinline__ bool before(const Cand &o) const
+    {
+        return k > o.k || (k == o.k && e < o.e);
+    }
+};
+
+// Batcher's odd-even merge sort of N (a power of two) candidates, first first.
+template <int N, typename C>
+__device__ __forceinline__ void sort_cands(C (&c)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        C &a = c[i + j], &b = c[i + j + k];
+                        const bool swap = b.before(a);
+                        const C t = a;
+                        a = swap ? b : a;
+                        b = swap ? t : b;
+                    }
+}
+
+// The two best of pairs (b1 >= b2) held by this lane and another.
+template <typename S>
+__device__ __forceinline__ void merge_best(S &b1, S &b2, S o1, S o2)
+{
+    const S lower = (b1 > o1) ? o1 : b1, second = (b2 > o2) ? b2 : o2;
+    b1 = (b1 > o1) ? b1 : o1;
+    b2 = (lower > second) ? lower : second;
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_value(float v)
+{
+    return __int_as_float(dpp0<CTRL, 0xf>(__float_as_int(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_value(double v)
+{
+    const long long u = __double_as_longlong(v);
+    const uint32_t lo = (uint32_t)dpp0<CTRL, 0xf>((int)(u & 0xffffffffll));
+    const uint32_t hi = (uint32_t)dpp0<CTRL, 0xf>((int)(u >> 32));
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 
 template <typename LT>
@@ -117,22 +231,34 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
     const int e0 = lane * NE;
     const S inf = (S)INFINITY;
 
-    // logits and bias of this lane's experts, all loads issued before any use
+    // logits and bias of this lane's experts, all loads issued before any use;
+    // a lane past the experts reads the last one's and drops them
+    struct __attribute__((packed, aligned(4))) Bias {
+        float v[NE];
+    };
     S l[NE], b[NE];
     const LT *row = static_cast<const LT *>(a.logits) + (int64_t)t * a.ld;
-    if (e0 + NE <= a.E) {
-        const Piece p = *reinterpret_cast<const Piece *>(row + e0);
+    {
+        Piece lp;
+        Bias bp;
+        if (e0 + NE <= a.E) {
+            lp = *reinterpret_cast<const Piece *>(row + e0);
+            if (a.bias)
+                bp = *reinterpret_cast<const Bias *>(a.bias + e0);
+        } else {
 #pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            l[j] = widen(p.v[j]);
-            b[j] = a.bias ? (S)a.bias[e0 + j] : (S)0;
+            for (int j = 0; j < NE; ++j)
+                lp.v[j] = row[min(e0 + j, a.E - 1)];
+            if (a.bias) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j)
+                    bp.v[j] = a.bias[min(e0 + j, a.E - 1)];
+            }
         }
-    } else {
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-            const bool in = e0 + j < a.E;
-            l[j] = in ? widen(row[e0 + j]) : -inf;
-            b[j] = (in && a.bias) ? (S)a.bias[e0 + j] : (S)0;
+            l[j] = (e0 + j < a.E) ? widen(lp.v[j]) : -inf;
+            b[j] = a.bias ? (S)bp.v[j] : (S)0;
         }
     }
     if constexpr (sizeof(LT) == 8) {
@@ -164,13 +290,14 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
             sum += p[j];
         }
         sum = wave_sum(sum);
+        const S by = (sum > (S)0) ? inverse(sum) : (S)0;
 #pragma unroll
         for (int j = 0; j < NE; ++j)
-            p[j] = (sum > (S)0) ? p[j] / sum : (S)0;
+            p[j] *= by;
     } else {
 #pragma unroll
         for (int j = 0; j < NE; ++j)
-            p[j] = (l[j] == l[j]) ? (S)1 / ((S)1 + exp_of(-l[j])) : (S)0;
+            p[j] = (l[j] == l[j]) ? inverse((S)1 + exp_of(-l[j])) : (S)0;
     }
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
@@ -180,38 +307,69 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
     }
 
     // the groups that stay: group g's bit at g*P, P neighbouring lanes (a power
-    // of two) working on one group; a group's values lie P further from the
-    // group before in LDS than their number, which spreads the banks
+    // of two) working on one group.  Where a group's experts are just P lanes'
+    // (256 experts in 8 groups: 8 lanes of 4) they begin with their own in
+    // registers; else the values go through LDS, a group's P further from the
+    // group before than their number, which spreads the banks (4096 tokens of
+    // 256 experts, launches in a graph: 6.1 us through LDS, 5.75 in registers).
     uint64_t stay = 0;
     int P = 1;
     const bool limited = a.topk_group < a.n_group;
     if (limited) {
-        while (2 * P * a.n_group <= 64)
-            P *= 2;
-        S *mine = lds[wave];
-#pragma unroll
-        for (int j = 0; j < NE; ++j)
-            if (e0 + j < a.E)
-                mine[e0 + j + (((uint32_t)(e0 + j) * a.gs_inv) >> 22) * P] = c[j];
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        const int g = lane / P, sub = lane & (P - 1);
         S b1 = -inf, b2 = -inf;
-        if (g < a.n_group) {
-            const S *mg = mine + g * ((int)a.gs + P);
-            for (int i = sub; i < (int)a.gs; i += P) {
-                const S v = mg[i];
-                b2 = (v > b1) ? b1 : (v > b2) ? v : b2;
-                b1 = (v > b1) ? v : b1;
+        if (a.lanes) {
+            P = a.lanes;
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                b2 = (c[j] > b1) ? b1 : (c[j] > b2) ? c[j] : b2;
+                b1 = (c[j] > b1) ? c[j] : b1;
+            }
+        } else {
+            while (2 * P * a.n_group <= 64)
+                P *= 2;
+            S *mine = lds[wave];
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                // the last place is nobody's: for what lies past the experts
+                const int at = e0 + j + (int)((((uint32_t)(e0 + j) * a.gs_inv) >> 22) * P);
+                mine[(e0 + j < a.E) ? at : 64 * NE + 63] = c[j];
+            }
+            wave_lds_sync();
+            const int g = lane / P;
+            if (g < a.n_group) {
+                const S *mg = mine + g * ((int)a.gs + P);
+                int i = lane & (P - 1);
+                for (; i + 3 * P < (int)a.gs; i += 4 * P) {     // four reads on their way
+                    S v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        v[u] = mg[i + u * P];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        b2 = (v[u] > b1) ? b1 : (v[u] > b2) ? v[u] : b2;
+                        b1 = (v[u] > b1) ? v[u] : b1;
+                    }
+                }
+                for (; i < (int)a.gs; i += P) {
+                    const S v = mg[i];
+                    b2 = (v > b1) ? b1 : (v > b2) ? v : b2;
+                    b1 = (v > b1) ? v : b1;
+                }
             }
         }
-        for (int o = 1; o < P; o *= 2) {
-            const S o1 = __shfl_xor(b1, o, 64), o2 = __shfl_xor(b2, o, 64);
-            const S lower = (b1 > o1) ? o1 : b1, second = (b2 > o2) ? b2 : o2;
-            b1 = (b1 > o1) ? b1 : o1;
-            b2 = (lower > second) ? lower : second;
-        }
+        const int g = lane / P, sub = lane & (P - 1);
+        // a group's lanes together: neighbours, pairs, then mirrored halves
+        // (once four or eight lanes agree, the mirror lies in the others)
+        if (P > 1)
+            merge_best(b1, b2, dpp_value<0xB1>(b1), dpp_value<0xB1>(b2));      // quad_perm 1,0,3,2
+        if (P > 2)
+            merge_best(b1, b2, dpp_value<0x4E>(b1), dpp_value<0x4E>(b2));      // quad_perm 2,3,0,1
+        if (P > 4)
+            merge_best(b1, b2, dpp_value<0x141>(b1), dpp_value<0x141>(b2));    // row_half_mirror
+        if (P > 8)
+            merge_best(b1, b2, dpp_value<0x140>(b1), dpp_value<0x140>(b2));    // row_mirror
+        if (P > 16)
+            merge_best(b1, b2, (S)__shfl_xor(b1, 16, 64), (S)__shfl_xor(b2, 16, 64));
         S score = (a.group_best == 2) ? b1 + b2 : b1;
         if (score != score)
             score = -inf;
@@ -222,44 +380,37 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
         }
         stay = __ballot(g < a.n_group && sub == 0 && rank < a.topk_group);
     }
-    Key key[NE], top = 0;
+    // this lane's candidates in the order of choice; p for whoever is chosen
+    Cand<Key> cand[NE];
+    S *mine = lds[wave];
+    wave_lds_sync();
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
         const uint32_t g = ((uint32_t)(e0 + j) * a.gs_inv) >> 22;
         const bool in = e0 + j < a.E && (!limited || ((stay >> (g * P)) & 1ull));
-        key[j] = in ? order_key(c[j]) : (Key)0;
-        top = max(top, key[j]);
+        cand[j].set(in ? order_key(c[j]) : (Key)0, e0 + j);
+        mine[e0 + j] = p[j];
     }
+    sort_cands(cand);
 
-    // k times the largest key, the lowest expert of it first
+    // k times the largest of the lanes' first candidates, the lowest lane's
+    // where they are equal; that lane moves on to its next
     int my_e = 0;
-    S my_p = 0, den = 0;
     for (int i = 0; i < a.k; ++i) {
-        const Key best = wave_top(top);
-        const int owner = __builtin_ctzll(__ballot(top == best));
-        int je = 0;
-        S jp = 0;
+        const Key best = wave_top(cand[0].key());
+        const int owner = __builtin_ctzll(__ballot(cand[0].key() == best));
+        const int e = __builtin_amdgcn_readlane(cand[0].expert(), owner);
+        my_e = (lane == i) ? e : my_e;
+        const bool won = lane == owner;
 #pragma unroll
-        for (int j = NE - 1; j >= 0; --j)
-            if (key[j] == best) {
-                je = e0 + j;
-                jp = p[j];
-            }
-        const int e = __builtin_amdgcn_readlane(je, owner);
-        const S pe = lane_value(jp, owner);
-        den += pe;
-        if (lane == i) {
-            my_e = e;
-            my_p = pe;
-        }
-        top = 0;
-#pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            if (e0 + j == e)
-                key[j] = 0;
-            top = max(top, key[j]);
-        }
+        for (int j = 0; j + 1 < NE; ++j)
+            cand[j] = won ? cand[j + 1] : cand[j];
+        if (won)
+            cand[NE - 1].set((Key)0, 0);
     }
+    wave_lds_sync();
+    const S my_p = (lane < a.k) ? mine[my_e] : (S)0;
+    const S den = wave_sum(my_p);
     if (lane < a.k) {
         const S v = a.renorm ? ((den > (S)0) ? my_p / den : (S)0) : my_p;
         a.idx[(int64_t)t * a.k + lane] = my_e;
@@ -267,21 +418,27 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
     }
 }
 
+template <typename LT, int NE>
+static void launch_select(SelectArgs a, hipStream_t st)
+{
+    const int lanes = (int)a.gs / NE;
+    a.lanes = (a.gs % NE == 0 && (lanes & (lanes - 1)) == 0) ? lanes : 0;
+    launch(select_kernel<LT, NE>, (unsigned)((a.T + 3) / 4), 256, 0, st, a);
+}
+
 template <typename LT>
 static hipError_t enqueue_select(const SelectArgs &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((a.T + 3) / 4);
-    const int ne = (a.E + 63) / 64;
-    if (ne <= 1)
-        launch(select_kernel<LT, 1>, grid, 256, 0, st, a);
-    else if (ne <= 2)
-        launch(select_kernel<LT, 2>, grid, 256, 0, st, a);
-    else if (ne <= 4)
-        launch(select_kernel<LT, 4>, grid, 256, 0, st, a);
-    else if (ne <= 8)
-        launch(select_kernel<LT, 8>, grid, 256, 0, st, a);
+    if (a.E <= 64)
+        launch_select<LT, 1>(a, st);
+    else if (a.E <= 128)
+        launch_select<LT, 2>(a, st);
+    else if (a.E <= 256)
+        launch_select<LT, 4>(a, st);
+    else if (a.E <= 512)
+        launch_select<LT, 8>(a, st);
     else
-        launch(select_kernel<LT, 16>, grid, 256, 0, st, a);
+        launch_select<LT, 16>(a, st);
     return hipGetLastError();
 }
 

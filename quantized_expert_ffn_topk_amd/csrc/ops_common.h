@@ -151,6 +151,14 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     *reinterpret_cast<bytes16_a4 *>(p + 4) = b;
 }
 
+// LDS written by lanes of a wave and read by others of the same wave
+__device__ __forceinline__ void wave_lds_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------
 // device: maximum and sum over a wave, in every lane.  DPP row shifts and
 // broadcasts bring them to lane 63 in six dependent VALU steps (the swizzles

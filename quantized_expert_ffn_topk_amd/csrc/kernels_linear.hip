@@ -188,8 +188,8 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
 
 // ---------------------------------------------------------------------------
 // Tiles: a block computes BT = 32*WT*FT tokens x BN = 32*WN*FN channels with
-// WT*WN waves of FT*FN 32x32 results, K in stages of 128 codes through two LDS
-// buffers, the next stage's rows on their way while one is multiplied.
+// WT*WN waves of FT*FN 32x32 results, K in stages of 128 codes through NB LDS
+// buffers, the next stages' rows on their way while one is multiplied.
 // An LDS row is 128 bytes, eight 16-byte pieces; piece c of row r sits at slot
 // c ^ (r/2 & 7): two rows fill the 64 banks once, so that 16 neighbouring rows'
 // reads of one piece fall on different banks.
@@ -197,6 +197,10 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
 // writing slot l%8 of row l/8, so the lane picks the global piece that belongs
 // there); needs rows of 16-byte alignment.  Otherwise they pass through
 // registers.  The last, partial stage always does (load_codes gives its zeros).
+// 256 x 256 tiles of 4096 x 24576 x 6144: 531 us, 2330 TOP/s (the library's int8
+// product 575), the matrix units busy 61 % of the cycles at 1.78 GHz.  Bound by
+// power: copies one and a half stages ahead instead of one took 2.6 % fewer
+// cycles at a 4 % lower clock, the same time; zeros for tokens are 17 % faster.
 // ---------------------------------------------------------------------------
 template <typename OT, bool DMA, int NB, int WT, int WN, int FT, int FN>
 __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, int tiles_t, int tiles_n)
@@ -502,13 +506,16 @@ static void launch_tiles(const LinArgs &a, hipStream_t st)
 // ---------------------------------------------------------------------------
 // Choice of a kernel.  Times in us on an MI355X, launches in a row.
 //
-// Stream: up to 64 tokens, and more where 32-channel x 64-token blocks still
-// find a CU each (256 x 2048 x 7168: 11.3, tiles 14.1; with one and a half
-// blocks per CU, 128 x 6144 x 6144, tiles win, 13.1 to 17.7).
-//  - Weight rows per block: 32; 16 where there are few channels (20 x 2048 x
-//    7168: 6.2 against 7.3) or at most 8 tokens (4 x 24576 x 6144: 22.8 against
-//    23.4); 48 with four waves from 24576 channels on, two blocks per CU, where
-//    the tokens are read less often (24 x 24576 x 6144: 26.7 against 28.1).
+// Stream: up to 64 tokens, and more where its blocks still find a CU each
+// (256 x 512 x 6144: 6.4, tiles 12.6; 256 x 2048 x 7168: 11.3, 14.1; with one
+// and a half blocks per CU, 128 x 6144 x 6144, tiles win, 13.1 to 17.7).
+//  - Blocks are as small as leaves each a CU: of the tokens 8, 16, 32 or 64, at
+//    most as many as there are, and 16 or 32 weight rows (64 x 2048 x 7168: 32
+//    tokens x 16 rows 6.9, 64 x 16 9.4, 64 x 32 11.1; 128 x 2048 x 6144, where
+//    the first would be 512 blocks: 9.5, 8.9, 10.2).  Up to 8 tokens 16 rows
+//    throughout (4 x 24576 x 6144: 22.8, with 32 rows 23.4).
+//  - 48 rows by four waves from 24576 channels on, two blocks per CU, where the
+//    tokens are read less often (24 x 24576 x 6144: 26.7, with 32 rows 28.1).
 //  - The non-temporal hint from 128 MiB of weights on, of which the 256 MiB
 //    last-level cache would not keep two (1 x 24576 x 6144: 23.2 with, 26.2
 //    without; 24: 26.7, 29.8).  Smaller weights may stay there from one call
@@ -519,14 +526,26 @@ static void launch_tiles(const LinArgs &a, hipStream_t st)
 // CU takes in (72 GB/s here, and 64 x 64 .. 128 x 256 tiles need 16 .. 48 KiB a
 // stage) or by its products (256 x 256), and a fixed part, the first stage's
 // way and the output.  Blocks go to 256 CUs; the tile with the smallest (blocks
-// per CU, rounded up) x (block's time) is taken.  Measured, 64x64 / 64x128 /
-// 128x128 / 128x256 / 256x256, K = 6144: 128 x 6144 13.1 / 18.6 / 25.2 / 36.9 / -;
-// 256 x 6144 21.5 / 19.1 / 25.3 / 37.0 / -; 512 x 6144 31.9 / 30.3 / 27.1 / 37.6 / -;
-// 1024 x 6144 63 / 51 / 55 / 42.8 / 65; 4096 x 24576 - / - / 664 / - / 535.
+// per CU, rounded up) x (block's time) is taken.  The two times of each tile
+// are fitted to 26 shapes; the tile taken is the fastest of the five on all of
+// them but two, and there within 10 %.  64x64 / 64x128 / 128x128 / 128x256 /
+// 256x256:
+//     128 x 6144 x 6144     13.1 / 18.6 / 25.2 / 36.9 / 61
+//     256 x 12288 x 6144    34.9 / 32.0 / 28.9 / 39.1 / 63
+//     600 x 8192 x 4096     37.2 / 36.0 / 39.8 / 30.7 / 47
+//    2048 x 24576 x 2048     222 /  176 /  180 /  135 / 109
+//    3000 x 8000 x 8000      362 /  296 /  259 /  208 / 217
 // Rows that are not 16-byte aligned pass through registers and cross a line
-// each, which costs all tiles alike (4096 x 24576 x 6144: 770; 561 where the
+// each, which costs all tiles alike (4096 x 24576 x 6144: 770; 535 where the
 // rows are aligned).
 // ---------------------------------------------------------------------------
+constexpr int64_t CUS = 256;
+
+static int64_t blocks_of(const LinArgs &a, int tokens, int rows)
+{
+    return (int64_t)((a.T + tokens - 1) / tokens) * ((a.N + rows - 1) / rows);
+}
+
 template <typename OT, int TC>
 static void enqueue_stream(const LinArgs &a, hipStream_t st)
 {
@@ -534,14 +553,14 @@ static void enqueue_stream(const LinArgs &a, hipStream_t st)
     if constexpr (TC == 1) {
         nt ? launch_stream<OT, true, 1, TC, 8>(a, st) : launch_stream<OT, false, 1, TC, 8>(a, st);
     } else {
-        if (nt && a.N >= 24576)
+        if (blocks_of(a, 8 * TC, 16) <= CUS)
+            launch_stream<OT, false, 1, TC, 8>(a, st);
+        else if (nt && a.N >= 24576)
             launch_stream<OT, true, 3, TC, 4>(a, st);
         else if (nt)
             launch_stream<OT, true, 2, TC, 8>(a, st);
-        else if (a.N > 4096 || a.T > 64)
-            launch_stream<OT, false, 2, TC, 8>(a, st);
         else
-            launch_stream<OT, false, 1, TC, 8>(a, st);
+            launch_stream<OT, false, 2, TC, 8>(a, st);
     }
 }
 
@@ -552,14 +571,13 @@ static void enqueue_tiles(const LinArgs &a, hipStream_t st)
         int bt, bn;
         double stage, fixed;                             // us of a block
     };
-    static constexpr Tile tile[5] = {{64, 64, 0.21, 1.0},   {64, 128, 0.36, 1.5}, {128, 128, 0.52, 4.0},
-                                     {128, 256, 0.82, 4.0}, {256, 256, 1.55, 8.0}};
+    static constexpr Tile tile[5] = {{64, 64, 0.20, 1.6},    {64, 128, 0.313, 1.9}, {128, 128, 0.49, 5.9},
+                                     {128, 256, 0.745, 7.1}, {256, 256, 1.27, 9.4}};
     int best = 0;
     double least = 0.0;
     for (int i = 0; i < 5; ++i) {
         const Tile &t = tile[i];
-        const int64_t blocks = (int64_t)((a.T + t.bt - 1) / t.bt) * ((a.N + t.bn - 1) / t.bn);
-        const double us = (double)((blocks + 255) / 256) * (t.stage * a.K / 128 + t.fixed);
+        const double us = (double)((blocks_of(a, t.bt, t.bn) + CUS - 1) / CUS) * (t.stage * a.K / 128 + t.fixed);
         if (i == 0 || us < least) {
             best = i;
             least = us;
@@ -583,9 +601,9 @@ static void enqueue_linear(const LinArgs &a, hipStream_t st)
         enqueue_stream<OT, 1>(a, st);
     else if (a.T <= 16)
         enqueue_stream<OT, 2>(a, st);
-    else if (a.T <= 32)
+    else if (a.T <= 32 || blocks_of(a, 32, 16) <= CUS)
         enqueue_stream<OT, 4>(a, st);
-    else if (a.T <= 64 || (int64_t)((a.T + 63) / 64) * ((a.N + 31) / 32) <= 256)
+    else if (a.T <= 64 || blocks_of(a, 64, 32) <= CUS)
         enqueue_stream<OT, 8>(a, st);
     else if (ops_aligned(a.q, 16) && ops_aligned(a.w, 16) && a.ldq % 16 == 0 && a.ldw % 16 == 0)
         enqueue_tiles<OT, true>(a, st);

@@ -275,17 +275,27 @@ def test_linear_many_tokens(T, N, K):
     check_linear(run_linear(q, s, w, ws, None, "f32"), q, s, w, ws, None, "f32")
 
 
-@pytest.mark.parametrize("T,N,K", [(200, 5003, 384), (1999, 2001, 1040), (2047, 4090, 640), (4001, 4093, 520)])
+@pytest.mark.parametrize("T,N,K", [(513, 1030, 512), (200, 5003, 384), (384, 6144, 2050), (1999, 2001, 1040),
+                                   (2047, 4090, 640), (4001, 4093, 520)])
 @pytest.mark.parametrize("pad", [0, 16, 3])
 def test_linear_every_tile_and_alignment(T, N, K, pad):
-    # shapes that spread over the chip as 64 x 128, 128 x 128, 128 x 256 and
-    # 256 x 256 tiles, whole and partial stages, aligned rows and others
+    # shapes that spread over the chip as 64 x 64, 64 x 128, 128 x 128, 128 x 256
+    # and 256 x 256 tiles, whole and partial stages, aligned rows and others
     q, s, w, ws, b = lin_inputs(6, T, N, K)
     check_linear(run_linear(q, s, w, ws, b, "bf16", pad), q, s, w, ws, b, "bf16")
     check_linear(run_linear(q, s, w, ws, None, "f32", pad), q, s, w, ws, None, "f32")
 
 
-@pytest.mark.parametrize("T,N,K", [(3, 6200, 21700), (12, 24600, 5505), (24, 24577, 5504), (40, 6200, 21700)])
+@pytest.mark.parametrize("T,N,K", [(7, 5001, 300), (12, 5001, 300), (24, 5001, 300), (50, 9001, 300), (64, 3000, 300)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (3, 5)])
+def test_linear_few_tokens_many_channels(T, N, K, pad, shift):
+    q, s, w, ws, b = lin_inputs(8, T, N, K)
+    check_linear(run_linear(q, s, w, ws, b, "bf16", pad, shift), q, s, w, ws, b, "bf16")
+    check_linear(run_linear(q, s, w, ws, None, "f32", pad, shift), q, s, w, ws, None, "f32")
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 6200, 21700), (12, 6200, 21700), (12, 24600, 5505), (24, 6200, 21700),
+                                   (24, 24577, 5504), (40, 6200, 21700), (40, 24577, 5504)])
 def test_linear_weights_beyond_the_cache(T, N, K):
     r = np.random.default_rng([7, T, N])
     q, w = r.integers(-128, 128, (T, K), dtype=np.int8), r.integers(-128, 128, (N, K), dtype=np.int8)

@@ -34,18 +34,21 @@ struct RowOut {
 };
 
 // silu(g)*u in fp32, from E = exp(-|g|) <= 1 so that nothing overflows:
-// g*u/(1+E) for g >= 0, g*u*E/(1+E) for g < 0.  E = 2^t with t = -|g|*log2(e)
-// as a rounded product and its remainder, so that the exponent's rounding does
-// not grow with |g|; the reciprocal is the hardware's (one unit in the last
-// place), of a number in [1,2].  Past |g| = 200 E is 0 either way.
+// g*u/(1+E) for g >= 0, g*u*E/(1+E) for g < 0.  E is the square of 2^t with
+// t = -|g|*log2(e)/2 as a rounded product and its remainder r, so that the
+// exponent's rounding does not grow with |g| and E reaches the subnormals,
+// which the hardware's 2^t itself does not; the reciprocal is the hardware's
+// (one unit in the last place), of a number in [1,2].  Past |g| = 200 E is 0
+// either way.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
-    const float L2E = 1.44269502f, L2E_LO = 1.92596303e-8f;   // log2(e) = L2E + L2E_LO
+    const float C = 0.72134751f, C_LO = 9.62981515e-9f;       // log2(e)/2 = C + C_LO
     const float a = fminf(fabsf(g), 200.0f);
-    const float t = -a * L2E;
-    const float r = fmaf(-a, L2E, -t) - a * L2E_LO;
-    float e = __builtin_exp2f(t);
-    e = fmaf(e, r * 0.693147181f, e);
+    const float t = -a * C;
+    const float r = fmaf(-a, C_LO, fmaf(-a, C, -t));
+    const float h = __builtin_amdgcn_exp2f(t);
+    float e = h * h;
+    e = fmaf(e, r * 1.386294361f, e);                         // (1 + r ln 2)^2
     const float d = __builtin_amdgcn_rcpf(1.0f + e);
     return g * ((g < 0.0f) ? e * d : d) * u;
 }
@@ -148,13 +151,14 @@ __device__ __forceinline__ void row_out(const RowOut &o, int t, int lane, bool l
     }
     if (!o.q)
         return;
-    uint32_t m = 0u;
+    // the maximum that keeps a NaN (v_maximum3_f32), then bits: NaN is largest
+    float big = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
-    m = row_max_u32<NT>(m, red);
+            big = __builtin_elementwise_maximum(big, fabsf(v[i][j]));
+    const uint32_t m = row_max_u32<NT>(__float_as_uint(big) & 0x7fffffffu, red);
     float s, pre, inv;
     row_scale(m, &s, &pre, &inv);
     if (!live)

@@ -247,27 +247,32 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
         for (int j = 0; j < FN; ++j)
             acc[i][j] = v16i{0};
     const int wt = wave / WN, wn = wave % WN;
-    // fragments of K step u (32 codes): two sets, one read while the other is multiplied
-    v4i av[2][FT], bv[2][FN];
+    // fragments: two sets, one read while the other is multiplied; of a K step
+    // (32 codes) each, or, where a step is a single product (WHOLE), of a
+    // stage's four
+    constexpr bool WHOLE = FT * FN == 1;
+    constexpr int US = WHOLE ? 4 : 1;
+    v4i av[2][US][FT], bv[2][US][FN];
     int slot[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
         slot[u] = (lane & 31) * 128 + ((2 * u + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
     const int a_at = 4096 * FT * wt, b_at = BT * 128 + 4096 * FN * wn;
     auto read = [&](int set, const uint8_t *buf, int u) {
+        const int k = WHOLE ? u : 0;
 #pragma unroll
         for (int i = 0; i < FT; ++i)
-            av[set][i] = *reinterpret_cast<const v4i *>(buf + slot[u] + a_at + 4096 * i);
+            av[set][k][i] = *reinterpret_cast<const v4i *>(buf + slot[u] + a_at + 4096 * i);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            bv[set][j] = *reinterpret_cast<const v4i *>(buf + slot[u] + b_at + 4096 * j);
+            bv[set][k][j] = *reinterpret_cast<const v4i *>(buf + slot[u] + b_at + 4096 * j);
     };
-    auto multiply = [&](int set) {
+    auto multiply = [&](int set, int k) {
 #pragma unroll
         for (int i = 0; i < FT; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bv[set][j], av[set][i], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bv[set][k][j], av[set][k][i], acc[i][j], 0, 0, 0);
     };
     // rows in registers on their way into LDS: two stages where there is room
     constexpr int RD = DMA ? 0 : (FT * FN <= 4) ? 2 : 1;
@@ -319,29 +324,16 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    // Stage st in four K steps, from buffer cur; step 0's fragments are in set 0
-    // on entry.  Before the last step is multiplied all of this stage has been
-    // read, so the waves meet there: from then on the next stage can be read
-    // and the NB-th from here copied over this one.  The stages' end (MORE =
-    // false) waits for all copies and sets out none past the last.
+    // The waves meet once per stage, when all of stage st has been read: from
+    // then on stage st + 1 can be read and stage st + LEAD be set out over this
+    // one.  The stages' end (MORE = false) waits for all copies and sets out
+    // none past the last.
     const int stages = a.K >> 7;
-    constexpr int LEAD = DMA ? NB : 1 + RD;              // the stage that stage st sets out: st + LEAD
-    auto stage = [&](auto more_, int st, uint8_t *cur, uint8_t *next, int set) {
-        constexpr bool MORE = decltype(more_)::value;
-        read(1, cur, 1);
-        multiply(0);
-        interleave();
-        read(0, cur, 2);
-        multiply(1);
-        interleave();
-        read(1, cur, 3);
-        if constexpr (!DMA)
-            land(next, set);
-        multiply(0);
-        interleave();
+    constexpr int LEAD = DMA ? NB : 1 + RD;
+    auto meet_at = [&](auto more_, int st) {
         if constexpr (!DMA) {
             meet_lds();
-        } else if constexpr (MORE) {
+        } else if constexpr (decltype(more_)::value) {
             meet(ahead);
         } else {
             if (st + NB - 1 < stages)
@@ -349,11 +341,54 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
             else
                 meet(all);
         }
-        read(0, next, 0);
-        if (MORE || st + LEAD < stages)
-            fetch(cur, set);
-        multiply(1);
-        interleave();
+    };
+    // WHOLE: stage st's fragments are in set `frag`; the next stage's are read
+    // while they are multiplied (read a K step ahead, a 64 x 64 tile's stage
+    // waited for LDS four times: 128 x 8192 x 6144 15.4 us, 13.7 like this).
+    // Else the stage is read a K step ahead, between the products, and the last
+    // step multiplied after the waves have met (with the next stage's 16 reads
+    // in front of its products, 128 x 128 tiles of 512 x 6144 x 6144 took 32.2
+    // us for 27.1).
+    auto stage = [&](auto more_, int st, uint8_t *cur, uint8_t *next, int set, int frag) {
+        constexpr bool MORE = decltype(more_)::value;
+        if constexpr (WHOLE) {
+            if constexpr (!DMA)
+                land(next, set);
+            meet_at(more_, st);
+            if (MORE || st + LEAD < stages)
+                fetch(cur, set);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                read(1 - frag, next, u);
+            __builtin_amdgcn_sched_barrier(0);           // all reads out first
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                multiply(frag, u);
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            read(1, cur, 1);
+            multiply(0, 0);
+            interleave();
+            read(0, cur, 2);
+            multiply(1, 0);
+            interleave();
+            read(1, cur, 3);
+            if constexpr (!DMA)
+                land(next, set);
+            multiply(0, 0);
+            interleave();
+            meet_at(more_, st);
+            read(0, next, 0);
+            if (MORE || st + LEAD < stages)
+                fetch(cur, set);
+            multiply(1, 0);
+            interleave();
+        }
+    };
+    auto read_first = [&]() {
+#pragma unroll
+        for (int u = 0; u < (WHOLE ? 4 : 1); ++u)
+            read(0, buf0, u);
     };
     if (stages > 0) {
         fetch(buf0, 0);
@@ -366,10 +401,15 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
             if constexpr (NB > 3)
                 if (3 < stages)
                     fetch(buf3, 0);
-            if (stages >= NB)
+            // each way reads for itself: joined before the reads, the compiler
+            // would wait for every copy there
+            if (stages >= NB) {
                 meet(std::integral_constant<int, NB - 1>());
-            else
+                read_first();
+            } else {
                 meet(all);
+                read_first();
+            }
         } else {
             land(buf0, 0);
             if (1 < stages)
@@ -377,30 +417,25 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
             if (RD > 1 && 2 < stages)
                 fetch(buf0, 0);
             meet_lds();
+            read_first();
         }
-        read(0, buf0, 0);
+        // stage i of a round of NB: buffer i, fragment set i % 2 (WHOLE), register
+        // set (i + 1) % RD, all known at compile time
         constexpr std::true_type more{};
         constexpr std::false_type end{};
-        constexpr int S1 = RD > 1 ? 1 : 0;               // register set of odd stages
+        static_assert(!WHOLE || NB % 2 == 0, "a round ends on the set it began with");
+        auto buf = [&](int i) { return i % NB == 0 ? buf0 : i % NB == 1 ? buf1 : i % NB == 2 ? buf2 : buf3; };
         int st = 0;
         for (; st + NB - 1 + LEAD < stages; st += NB) {
-            stage(more, st, buf0, buf1, S1);
-            stage(more, st, buf1, NB > 2 ? buf2 : buf0, 0);
-            if constexpr (NB > 2)
-                stage(more, st, buf2, NB > 3 ? buf3 : buf0, 0);
-            if constexpr (NB > 3)
-                stage(more, st, buf3, buf0, 0);
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                stage(more, st + i, buf(i), buf(i + 1), RD > 1 ? (i + 1) % 2 : 0, i % 2);
         }
         for (; st < stages; st += NB) {
-            stage(end, st, buf0, buf1, S1);
-            if (st + 1 < stages)
-                stage(end, st + 1, buf1, NB > 2 ? buf2 : buf0, 0);
-            if constexpr (NB > 2)
-                if (st + 2 < stages)
-                    stage(end, st + 2, buf2, NB > 3 ? buf3 : buf0, 0);
-            if constexpr (NB > 3)
-                if (st + 3 < stages)
-                    stage(end, st + 3, buf3, buf0, 0);
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                if (st + i < stages)
+                    stage(end, st + i, buf(i), buf(i + 1), RD > 1 ? (i + 1) % 2 : 0, i % 2);
         }
     }
     const bool tail = (a.K & 127) != 0;
@@ -415,7 +450,7 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             read(u & 1, buf0, u);
-            multiply(u & 1);
+            multiply(u & 1, WHOLE ? u : 0);
         }
     }
 

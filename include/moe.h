@@ -265,7 +265,7 @@ moe_status moe_swiglu_quant(const void *gu, int32_t gu_dtype, int64_t ld, int32_
  * ws [N]; bias [N] may be NULL.  Codes are any int8 values; the sum is exact
  * (int32, 1 <= K <= 131071) and the rest fp32 in that order, so the bits of out
  * depend on nothing but the inputs.  out is MOE_DT_F32 or MOE_DT_BF16 (rounded
- * to nearest even).  1 <= N <= 2^20. */
+ * to nearest even).  1 <= N <= 2^20, T*N <= 2^38. */
 moe_status moe_linear_int8(const int8_t *q, int64_t ldq, const float *s, int32_t T,
                            const int8_t *w, int64_t ldw, const float *ws, const float *bias,
                            int32_t N, int32_t K, void *out, int32_t out_dtype, int64_t ldo,

@@ -78,6 +78,16 @@ class _Norm:
             raise ValueError("x and residual must be on %s" % self.dev)
         return T, ldx, ldr
 
+    def _on(self, stream):
+        """The device, and torch's current stream: what is allocated inside belongs
+        to the stream that writes it."""
+        t = self.torch
+        if stream is None:
+            return t.cuda.stream(t.cuda.default_stream(self.dev))
+        if isinstance(stream, int):
+            return t.cuda.stream(t.cuda.ExternalStream(stream, device=self.dev))
+        return t.cuda.stream(stream)
+
     def _norm(self, x, residual, y, q, s, stream):
         T, ldx, ldr = self._check(x, residual)
         h = self.torch.empty((T, self.H), dtype=residual.dtype, device=self.dev)
@@ -113,17 +123,18 @@ class DenseFFN(_Norm):
         self.qh, self.sh = e(n, F, dt=t.int8), e(n, dt=t.float32)
 
     def forward(self, x, residual, stream=None):
-        """(output [T, H], new residual [T, H]); enqueued on `stream`, which the
-        inputs must be ready on and the outputs are made on.  One call at a
-        time: the intermediate rows are the object's own."""
+        """(output [T, H], new residual [T, H]); enqueued on `stream` (None: the
+        null stream), which the inputs must be ready on and the outputs belong
+        to.  One call at a time: the intermediate rows are the object's own."""
         H, F = self.H, self.F
-        T, h = self._norm(x, residual, None, self.q, self.s, stream)
-        out = self.torch.empty((T, H), dtype=self.out_dtype, device=self.dev)
-        abi.moe_linear_int8(self.q, H, self.s, T, self.gate_up, H, self.s_gu, None, 2 * F, H, self.gu,
-                            abi.DT_BF16, 2 * F, stream)
-        abi.moe_swiglu_quant(self.gu, abi.DT_BF16, 2 * F, T, F, None, 0, self.qh, F, self.sh, stream)
-        abi.moe_linear_int8(self.qh, F, self.sh, T, self.down, F, self.s_dn, None, H, F, out,
-                            _dtype(out), H, stream)
+        with self._on(stream):
+            T, h = self._norm(x, residual, None, self.q, self.s, stream)
+            out = self.torch.empty((T, H), dtype=self.out_dtype, device=self.dev)
+            abi.moe_linear_int8(self.q, H, self.s, T, self.gate_up, H, self.s_gu, None, 2 * F, H, self.gu,
+                                abi.DT_BF16, 2 * F, stream)
+            abi.moe_swiglu_quant(self.gu, abi.DT_BF16, 2 * F, T, F, None, 0, self.qh, F, self.sh, stream)
+            abi.moe_linear_int8(self.qh, F, self.sh, T, self.down, F, self.s_dn, None, H, F, out,
+                                _dtype(out), H, stream)
         return out, h
 
 
@@ -147,10 +158,11 @@ class MoEFFN(_Norm):
     def forward(self, x, residual, stream=None):
         """As DenseFFN.forward; the chosen experts and their weights are in
         idx[:T] and w[:T] afterwards."""
-        T, h = self._norm(x, residual, self.y, None, None, stream)
         odt = self.torch.bfloat16 if self.layer.desc.out_dtype == abi.DT_BF16 else self.torch.float32
-        out = self.torch.empty((T, self.H), dtype=odt, device=self.dev)
-        abi.moe_router_topk_grouped(self.layer.ctx, self.route, self.y, T, self.layer.weights, self.idx,
-                                    self.w, stream)
-        abi.moe_expert_ffn(self.layer.ctx, self.y, T, self.layer.weights, self.idx, self.w, out, stream)
+        with self._on(stream):
+            T, h = self._norm(x, residual, self.y, None, None, stream)
+            out = self.torch.empty((T, self.H), dtype=odt, device=self.dev)
+            abi.moe_router_topk_grouped(self.layer.ctx, self.route, self.y, T, self.layer.weights, self.idx,
+                                        self.w, stream)
+            abi.moe_expert_ffn(self.layer.ctx, self.y, T, self.layer.weights, self.idx, self.w, out, stream)
         return out, h

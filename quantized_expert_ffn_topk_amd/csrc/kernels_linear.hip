@@ -659,6 +659,8 @@ extern "C" moe_status moe_linear_int8(const int8_t *q, int64_t ldq, const float 
         return fail(MOE_E_INVAL, "T=%d out of range [0, 2^20]", T);
     if (N < 1 || N > (1 << 20))
         return fail(MOE_E_INVAL, "N=%d must be in [1, 2^20]", N);
+    if ((int64_t)T * N > (1ll << 38))                // the launch's limit on threads
+        return fail(MOE_E_INVAL, "T*N=%lld above 2^38", (long long)T * N);
     // 2^14 per product at most: the int32 sum holds 131071 of them
     if (K < 1 || K > 131071)
         return fail(MOE_E_INVAL, "K=%d must be in [1, 131071]", K);

@@ -107,6 +107,10 @@ def test_halves_on_a_side_stream_and_of_no_tokens():
         got = d.forward(x, r, side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+    side.wait_stream(torch.cuda.current_stream())
+    got = d.forward(x, r, side.cuda_stream)              # the raw handle
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
     y, h = d.forward(x[:0], r[:0])
     assert y.shape == (0, 256) and h.shape == (0, 256)
 

@@ -45,7 +45,7 @@ def test_swiglu_refusals(bad):
 
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(s=None), dict(w=None), dict(ws=None), dict(out=None), dict(T=-1),
-    dict(T=(1 << 20) + 1), dict(N=0), dict(N=(1 << 20) + 1), dict(K=0), dict(K=131072), dict(ldq=63),
+    dict(T=(1 << 20) + 1), dict(T=1 << 20, N=1 << 19, ldo=1 << 19), dict(N=0), dict(N=(1 << 20) + 1), dict(K=0), dict(K=131072), dict(ldq=63),
     dict(ldw=63), dict(ldo=31), dict(out_dtype=2), dict(s=P + 2), dict(ws=P + 1), dict(bias=P + 2),
     dict(out=P + 1), dict(out_dtype=0, out=P + 2)])
 def test_linear_refusals(bad):

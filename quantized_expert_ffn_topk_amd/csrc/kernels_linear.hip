@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
 // power: copies one and a half stages ahead instead of one took 2.6 % fewer
 // cycles at a 4 % lower clock, the same time; zeros for tokens are 17 % faster.
 // ---------------------------------------------------------------------------
-template <typename OT, bool DMA, int NB, int WT, int WN, int FT, int FN>
+template <typename OT, bool DMA, int AHEAD, int WT, int WN, int FT, int FN>
 __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, int tiles_t, int tiles_n)
 {
     constexpr int NW = WT * WN, BT = 32 * WT * FT, BN = 32 * WN * FN;
@@ -212,6 +212,7 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole copies per wave");
     // the buffers are objects of their own: the compiler then knows that reads
     // of one do not wait for copies into another
+    constexpr int NB = DMA ? AHEAD : 2;
     static_assert(NB >= 2 && NB <= 4, "two to four buffers");
     __shared__ __align__(128) uint8_t buf0[BUF];
     __shared__ __align__(128) uint8_t buf1[BUF];
@@ -274,10 +275,9 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
             for (int j = 0; j < FN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bv[set][k][j], av[set][k][i], acc[i][j], 0, 0, 0);
     };
-    // rows in registers on their way into LDS: two stages where there is room
-    constexpr int RD = DMA ? 0 : (FT * FN <= 4) ? 2 : 1;
-    static_assert(DMA || NB == 2, "through registers two buffers do");
-    v4i reg[RD ? RD : 1][DMA ? 1 : CP];
+    constexpr int RD = DMA ? 0 : AHEAD;                  // stages in registers on their way into LDS
+    constexpr int SETS = DMA ? 1 : RD;
+    v4i reg[SETS][DMA ? 1 : CP];
     auto fetch = [&](uint8_t *buf, int set) {            // sets out the next whole stage
 #pragma unroll
         for (int i = 0; i < CP; ++i) {
@@ -412,30 +412,31 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
             }
         } else {
             land(buf0, 0);
-            if (1 < stages)
-                fetch(buf1, RD - 1);
-            if (RD > 1 && 2 < stages)
-                fetch(buf0, 0);
+#pragma unroll
+            for (int i = 1; i <= RD; ++i)
+                if (i < stages)
+                    fetch(buf0, i % SETS);
             meet_lds();
             read_first();
         }
-        // stage i of a round of NB: buffer i, fragment set i % 2 (WHOLE), register
+        // stage i of a round: buffer i % NB, fragment set i % 2 (WHOLE), register
         // set (i + 1) % RD, all known at compile time
+        constexpr int ROUND = DMA ? NB : RD % 2 ? 2 * RD : RD;
         constexpr std::true_type more{};
         constexpr std::false_type end{};
-        static_assert(!WHOLE || NB % 2 == 0, "a round ends on the set it began with");
+        static_assert(!WHOLE || ROUND % 2 == 0, "a round ends on the set it began with");
         auto buf = [&](int i) { return i % NB == 0 ? buf0 : i % NB == 1 ? buf1 : i % NB == 2 ? buf2 : buf3; };
         int st = 0;
-        for (; st + NB - 1 + LEAD < stages; st += NB) {
+        for (; st + ROUND - 1 + LEAD < stages; st += ROUND) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
-                stage(more, st + i, buf(i), buf(i + 1), RD > 1 ? (i + 1) % 2 : 0, i % 2);
+            for (int i = 0; i < ROUND; ++i)
+                stage(more, st + i, buf(i), buf(i + 1), (i + 1) % SETS, i % 2);
         }
-        for (; st < stages; st += NB) {
+        for (; st < stages; st += ROUND) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+            for (int i = 0; i < ROUND; ++i)
                 if (st + i < stages)
-                    stage(end, st + i, buf(i), buf(i + 1), RD > 1 ? (i + 1) % 2 : 0, i % 2);
+                    stage(end, st + i, buf(i), buf(i + 1), (i + 1) % SETS, i % 2);
         }
     }
     const bool tail = (a.K & 127) != 0;
@@ -530,25 +531,29 @@ static void launch_stream(const LinArgs &a, hipStream_t st)
     launch(linear_stream_kernel<OT, NT, RT, TC, W>, grid, 64 * W, 0, st, a);
 }
 
-template <typename OT, bool DMA, int NB, int WT, int WN, int FT, int FN>
+template <typename OT, bool DMA, int AHEAD, int WT, int WN, int FT, int FN>
 static void launch_tiles(const LinArgs &a, hipStream_t st)
 {
     const int tt = (a.T + 32 * WT * FT - 1) / (32 * WT * FT), tn = (a.N + 32 * WN * FN - 1) / (32 * WN * FN);
     const unsigned grid = ((unsigned)tt * tn + 7) / 8 * 8;
-    launch(linear_tiles_kernel<OT, DMA, NB, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
+    launch(linear_tiles_kernel<OT, DMA, AHEAD, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
 }
 
 // ---------------------------------------------------------------------------
 // Choice of a kernel.  Times in us on an MI355X, launches in a row.
 //
 // Stream: up to 64 tokens, and more where its blocks still find a CU each
-// (256 x 512 x 6144: 6.4, tiles 12.6; 256 x 2048 x 7168: 11.3, 14.1; with one
-// and a half blocks per CU, 128 x 6144 x 6144, tiles win, 13.1 to 17.7).
-//  - Blocks are as small as leaves each a CU: of the tokens 8, 16, 32 or 64, at
-//    most as many as there are, and 16 or 32 weight rows (64 x 2048 x 7168: 32
-//    tokens x 16 rows 6.9, 64 x 16 9.4, 64 x 32 11.1; 128 x 2048 x 6144, where
-//    the first would be 512 blocks: 9.5, 8.9, 10.2).  Up to 8 tokens 16 rows
-//    throughout (4 x 24576 x 6144: 22.8, with 32 rows 23.4).
+// (256 x 512 x 6144: 6.4, tiles 12.0; 256 x 2048 x 7168: 11.3, 13.3; with one
+// and a half blocks per CU, 128 x 6144 x 6144, tiles win, 12.7 to 20.3).
+//  - Blocks are as small as leaves each a CU: 8 tokens, 16, 32 or 64, at most as
+//    many as there are, and 16, 32 or 48 weight rows (64 x 256 x 6144 in 16
+//    tokens x 16 rows 4.4, 32 x 16 5.2; 64 x 2048 x 7168 in 32 x 16 6.9, 64 x 16
+//    9.3; 171 x 896 x 5744 in 32 x 32 9.6, 64 x 32 13.7; 1748 x 192 x 8000 in
+//    32 x 48 14.3, 64 x 32 18.6; 32 x 8448 x 6144, 11.0, and in 32 x 32 14.8).
+//  - Up to 8 tokens 16 rows throughout (4 x 24576 x 6144: 22.8, with 32 rows
+//    23.4), in 16 waves where a CU has one block (1 x 512 x 12288: 5.5, with 8
+//    waves 6.5; 8 x 2048 x 7168: 5.0, 5.4; 1 x 12288 x 2048, three blocks: 7.3,
+//    6.2).
 //  - 48 rows by four waves from 24576 channels on, two blocks per CU, where the
 //    tokens are read less often (24 x 24576 x 6144: 26.7, with 32 rows 28.1).
 //  - The non-temporal hint from 128 MiB of weights on, of which the 256 MiB
@@ -558,21 +563,27 @@ static void launch_tiles(const LinArgs &a, hipStream_t st)
 //    from memory; with the hint 11.7 from either.
 //
 // Tiles: a block's time is about its stages of 128 codes, each bound by what a
-// CU takes in (72 GB/s here, and 64 x 64 .. 128 x 256 tiles need 16 .. 48 KiB a
-// stage) or by its products (256 x 256), and a fixed part, the first stage's
-// way and the output.  Blocks go to 256 CUs; the tile with the smallest (blocks
-// per CU, rounded up) x (block's time) is taken.  The two times of each tile
-// are fitted to 26 shapes; the tile taken is the fastest of the five on all of
-// them but two, and there within 10 %.  64x64 / 64x128 / 128x128 / 128x256 /
+// CU takes in (some 40 bytes a clock; 64 x 64 .. 192 x 128 tiles need 16 .. 40
+// KiB a stage) or by its products (256 x 256), and a fixed part, the first
+// stage's way and the output.  Blocks go to 256 CUs in rounds; two of the
+// smallest tiles fit a CU and share their fixed parts, and one that is alone
+// takes longer per stage.  The tile whose rounds take least is taken.  The times
+// are fitted to 139 shapes of 65 to 4096 tokens, 64 to 12288 long: the tile
+// taken is on average 0.2 % slower than the fastest of the eight, at most 8 %.
+// (With 64x64, 64x128, 128x128, 128x256 and 256x256 alone the fastest are 4.5 %
+// slower.)  64x64 / 64x128 / 96x128 / 128x128 / 192x128 / 128x256 / 192x256 /
 // 256x256:
-//     128 x 6144 x 6144     13.1 / 18.6 / 25.2 / 36.9 / 61
-//     256 x 12288 x 6144    34.9 / 32.0 / 28.9 / 39.1 / 63
-//     600 x 8192 x 4096     37.2 / 36.0 / 39.8 / 30.7 / 47
-//    2048 x 24576 x 2048     222 /  176 /  180 /  135 / 109
-//    3000 x 8000 x 8000      362 /  296 /  259 /  208 / 217
-// Rows that are not 16-byte aligned pass through registers and cross a line
-// each, which costs all tiles alike (4096 x 24576 x 6144: 770; 535 where the
-// rows are aligned).
+//    128 x  6144 x 6144   12.7 / 18.5 / 22.0 / 25.1 / 29.9 / 36.9 / 48.4 / 60.8
+//    256 x 12288 x 6144   30.9 / 31.6 / 45.0 / 28.1 / 33.6 / 38.0 / 49.5 / 61.7
+//    451 x  4992 x 2688   16.0 / 15.4 / 14.3 / 14.8 / 17.3 / 20.2 / 26.6 / 33.7
+//    520 x  9856 x 3008   39.2 / 35.2 / 34.0 / 36.3 / 24.8 / 27.6 / 35.5 / 40.3
+//    600 x  8192 x 4096   33.5 / 34.2 / 34.1 / 38.4 / 27.7 / 28.5 / 36.0 / 44.5
+//   1309 x  7360 x 1344   37.2 / 30.8 / 38.8 / 34.8 / 25.8 / 31.3 / 21.6 / 26.1
+//   2048 x 24576 x 2048    217 /  173 /  192 /  176 /  145 /  131 /  128 /  106
+//   3000 x  8000 x 8000    361 /  294 /  311 /  252 /  232 /  206 /  203 /  213
+// Rows that are not 16-byte aligned pass through registers: each piece crosses a
+// line (a quarter more time), and at odd addresses another quarter (128 x 6144 x
+// 6144: 12.7 aligned, 24 at odd strides; 4096 x 24576 x 6144: 535, 770).
 // ---------------------------------------------------------------------------
 constexpr int64_t CUS = 256;
 
@@ -585,11 +596,19 @@ template <typename OT, int TC>
 static void enqueue_stream(const LinArgs &a, hipStream_t st)
 {
     const bool nt = (int64_t)a.N * a.K > (128 << 20);
+    const bool one = blocks_of(a, 8 * TC, 16) <= CUS;    // of the smallest blocks a CU each
     if constexpr (TC == 1) {
-        nt ? launch_stream<OT, true, 1, TC, 8>(a, st) : launch_stream<OT, false, 1, TC, 8>(a, st);
+        if (one)
+            launch_stream<OT, false, 1, TC, 16>(a, st);
+        else
+            nt ? launch_stream<OT, true, 1, TC, 8>(a, st) : launch_stream<OT, false, 1, TC, 8>(a, st);
+    } else if constexpr (TC == 8) {
+        nt ? launch_stream<OT, true, 2, TC, 8>(a, st) : launch_stream<OT, false, 2, TC, 8>(a, st);
     } else {
-        if (blocks_of(a, 8 * TC, 16) <= CUS)
+        if (one)
             launch_stream<OT, false, 1, TC, 8>(a, st);
+        else if (blocks_of(a, 8 * TC, 32) > CUS && blocks_of(a, 8 * TC, 48) <= CUS)
+            launch_stream<OT, false, 3, TC, 8>(a, st);
         else if (nt && a.N >= 24576)
             launch_stream<OT, true, 3, TC, 4>(a, st);
         else if (nt)
@@ -603,29 +622,36 @@ template <typename OT, bool DMA>
 static void enqueue_tiles(const LinArgs &a, hipStream_t st)
 {
     struct Tile {
-        int bt, bn;
-        double stage, fixed;                             // us of a block
+        int bt, bn, fit;                                 // blocks of it that fit a CU
+        double stage, fixed, alone;                      // us, see above
     };
-    static constexpr Tile tile[5] = {{64, 64, 0.20, 1.6},    {64, 128, 0.313, 1.9}, {128, 128, 0.49, 5.9},
-                                     {128, 256, 0.745, 7.1}, {256, 256, 1.27, 9.4}};
+    static constexpr Tile tile[8] = {
+        {64, 64, 2, 0.211, 2.4, 0.113},  {64, 128, 2, 0.313, 3.4, 0.079}, {96, 128, 1, 0.548, 3.8, 0.0},
+        {128, 128, 1, 0.514, 6.7, 0.0},  {192, 128, 1, 0.533, 6.4, 0.0},  {128, 256, 1, 0.849, 6.9, 0.0},
+        {192, 256, 1, 0.992, 7.1, 0.0},  {256, 256, 1, 1.298, 9.4, 0.0}};
     int best = 0;
     double least = 0.0;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const Tile &t = tile[i];
-        const double us = (double)((blocks_of(a, t.bt, t.bn) + CUS - 1) / CUS) * (t.stage * a.K / 128 + t.fixed);
+        const int64_t n = (blocks_of(a, t.bt, t.bn) + CUS - 1) / CUS;
+        const double k = a.K / 128.0, alone = n % t.fit ? t.alone : 0.0;
+        const double us = (n * t.stage + alone) * k + (n + t.fit - 1) / t.fit * t.fixed;
         if (i == 0 || us < least) {
             best = i;
             least = us;
         }
     }
-    // through registers two buffers do; copies go three or four stages ahead
-    // where the LDS has room
+    // copies: as many stages ahead as the LDS has room for, two blocks of the
+    // smallest tiles to a CU; registers: as many as they hold
     switch (best) {
-    case 0: launch_tiles<OT, DMA, DMA ? 4 : 2, 2, 2, 1, 1>(a, st); break;
-    case 1: launch_tiles<OT, DMA, DMA ? 3 : 2, 2, 2, 1, 2>(a, st); break;
-    case 2: launch_tiles<OT, DMA, DMA ? 3 : 2, 2, 2, 2, 2>(a, st); break;
-    case 3: launch_tiles<OT, DMA, DMA ? 3 : 2, 2, 4, 2, 2>(a, st); break;
-    default: launch_tiles<OT, DMA, 2, 2, 4, 4, 2>(a, st); break;
+    case 0: launch_tiles<OT, DMA, DMA ? 4 : 3, 2, 2, 1, 1>(a, st); break;
+    case 1: launch_tiles<OT, DMA, 3, 2, 2, 1, 2>(a, st); break;
+    case 2: launch_tiles<OT, DMA, 3, 1, 4, 3, 1>(a, st); break;
+    case 3: launch_tiles<OT, DMA, 3, 2, 2, 2, 2>(a, st); break;
+    case 4: launch_tiles<OT, DMA, 3, 2, 4, 3, 1>(a, st); break;
+    case 5: launch_tiles<OT, DMA, 3, 2, 4, 2, 2>(a, st); break;
+    case 6: launch_tiles<OT, DMA, 2, 2, 4, 3, 2>(a, st); break;
+    default: launch_tiles<OT, DMA, DMA ? 2 : 1, 2, 4, 4, 2>(a, st); break;
     }
 }
 
@@ -634,9 +660,9 @@ static void enqueue_linear(const LinArgs &a, hipStream_t st)
 {
     if (a.T <= 8)
         enqueue_stream<OT, 1>(a, st);
-    else if (a.T <= 16)
+    else if (a.T <= 16 || blocks_of(a, 16, 16) <= CUS)
         enqueue_stream<OT, 2>(a, st);
-    else if (a.T <= 32 || blocks_of(a, 32, 16) <= CUS)
+    else if (a.T <= 32 || blocks_of(a, 32, 48) <= CUS)
         enqueue_stream<OT, 4>(a, st);
     else if (a.T <= 64 || blocks_of(a, 64, 32) <= CUS)
         enqueue_stream<OT, 8>(a, st);

@@ -286,6 +286,31 @@ def test_linear_every_tile_and_alignment(T, N, K, pad):
     check_linear(run_linear(q, s, w, ws, None, "f32", pad), q, s, w, ws, None, "f32")
 
 
+# shapes that fill the chip best as 64 x 64, 64 x 128 or (longer K) 96 x 128,
+# 192 x 128, 128 x 256, 192 x 256, 256 x 256 and 128 x 128 tiles, with every
+# remainder of the stages' count that the kernels' rounds distinguish
+@pytest.mark.parametrize("T,N,K", [(T, N, K) for T, N in ((66, 4170), (259, 6579))
+                                   for K in (100, 256, 384, 520, 640, 768, 896, 1032, 1152, 1300, 1664)] +
+                         [(T, N, K) for T, N in ((516, 7243), (780, 6620), (1030, 7200), (1545, 7250))
+                          for K in (272, 640, 1032)] + [(110, 20001, K) for K in (4112, 4480, 4608)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_linear_tiles_at_every_count_of_stages(T, N, K, pad):
+    q, s, w, ws, b = lin_inputs(9, T, N, K)
+    od = "bf16" if K % 256 else "f32"
+    check_linear(run_linear(q, s, w, ws, b, od, pad), q, s, w, ws, b, od)
+
+
+# weights split among 8 and 16 waves, in 16, 32 and 48 rows; tokens in 8, 16, 32
+# and 64, also more of them than one block takes
+@pytest.mark.parametrize("T,N,K", [(1, 4096, 1100), (8, 4100, 6100), (16, 9001, 1500), (32, 9001, 1500), (100, 300, 4500),
+                                   (70, 1999, 1500), (100, 2500, 1500), (500, 700, 1500), (210, 1900, 1500)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_linear_splits_of_a_weight_stream(T, N, K, pad):
+    q, s, w, ws, b = lin_inputs(10, T, N, K)
+    check_linear(run_linear(q, s, w, ws, b, "bf16", pad), q, s, w, ws, b, "bf16")
+    check_linear(run_linear(q, s, w, ws, None, "f32", pad), q, s, w, ws, None, "f32")
+
+
 @pytest.mark.parametrize("T,N,K", [(7, 5001, 300), (12, 5001, 300), (24, 5001, 300), (50, 9001, 300), (64, 3000, 300)])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (3, 5)])
 def test_linear_few_tokens_many_channels(T, N, K, pad, shift):

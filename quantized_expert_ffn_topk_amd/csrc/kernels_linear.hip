@@ -19,26 +19,30 @@ struct LinArgs {
     int T, N, K;
 };
 
-// 16 codes of a row at k (a multiple of 16), zeros past K, at any alignment.
-// The piece that passes the row's end is read as the row's last 16 bytes and
-// shifted down; rows shorter than 16 byte by byte.
+__device__ __forceinline__ v4i load16(const int8_t *p)
+{
+    const bytes16_a1 b = *reinterpret_cast<const bytes16_a1 *>(p);
+    return v4i{(int)b.d[0], (int)b.d[1], (int)b.d[2], (int)b.d[3]};
+}
+
+// 16 codes of a row at k (a multiple of 16), zeros past K, at any alignment, with
+// one load: what passes the row's end is read as the row's last 16 bytes and
+// shifted down.  (Rows shorter than 16 byte by byte.)
 __device__ __forceinline__ v4i load_codes(const int8_t *row, int k, int K)
 {
     v4i v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        const bytes16_a1 b = *reinterpret_cast<const bytes16_a1 *>(row + k);
-        v = v4i{(int)b.d[0], (int)b.d[1], (int)b.d[2], (int)b.d[3]};
-    } else if (k < K) {
-        if (K >= 16) {
-            const unsigned __int128 b = __builtin_bit_cast(
-                unsigned __int128, *reinterpret_cast<const bytes16_a1 *>(row + K - 16));
-            v = __builtin_bit_cast(v4i, b >> (8 * (k + 16 - K)));
-        } else {
-            unsigned __int128 b = 0;
-            for (int j = 0; j < K; ++j)                      // k is 0 here
-                b |= (unsigned __int128)(uint8_t)row[j] << (8 * j);
-            v = __builtin_bit_cast(v4i, b);
-        }
+    if (K >= 16) {
+        if (k < K)
+            v = load16(row + min(k, K - 16));
+        const bool past = k < K && k + 16 > K;
+        if (__ballot(past))
+            v = __builtin_bit_cast(v4i, __builtin_bit_cast(unsigned __int128, v) >>
+                                            (past ? 8 * (k + 16 - K) : 0));
+    } else {
+        unsigned __int128 b = 0;
+        for (int j = k; j < K; ++j)                          // k is 0, or past the row
+            b |= (unsigned __int128)(uint8_t)row[j] << (8 * j);
+        v = __builtin_bit_cast(v4i, b);
     }
     return v;
 }
@@ -67,11 +71,6 @@ __device__ __forceinline__ void store_out(const LinArgs &a, int t, int n, int ac
 // l%16.  LDS rows are swizzled as in the tiles below.
 // NT: weights read with the non-temporal hint.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ v4i load16(const int8_t *p)
-{
-    const bytes16_a1 b = *reinterpret_cast<const bytes16_a1 *>(p);
-    return v4i{(int)b.d[0], (int)b.d[1], (int)b.d[2], (int)b.d[3]};
-}
 __device__ __forceinline__ v4i load16_stream(const int8_t *p)
 {
     typedef int v4i_a1 __attribute__((ext_vector_type(4), aligned(1)));
@@ -443,10 +442,8 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     if (tail) {
         const int k = 128 * stages + 16 * piece;         // src has come this far
 #pragma unroll
-        for (int i = 0; i < CP; ++i) {
+        for (int i = 0; i < CP; ++i)
             *reinterpret_cast<v4i *>(buf0 + lds_at(i) + 16 * lane) = load_codes(src[i] - k, k, a.K);
-            asm volatile("" ::: "memory");               // one at a time: it is a single stage
-        }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < 4; ++u) {

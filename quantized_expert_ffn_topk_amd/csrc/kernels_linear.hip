@@ -185,6 +185,15 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
     }
 }
 
+// 16 bytes of each lane from memory to LDS at 16 times the lane, by the load
+// unit; NT_BIT 2: with the non-temporal hint
+template <int NT_BIT>
+__device__ __forceinline__ void copy16(const int8_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 16, 0, NT_BIT);
+}
+
 // ---------------------------------------------------------------------------
 // Tiles: a block computes BT = 32*WT*FT tokens x BN = 32*WN*FN channels with
 // WT*WN waves of FT*FN 32x32 results, K in stages of 128 codes through NB LDS
@@ -201,7 +210,7 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
 // power: copies one and a half stages ahead instead of one took 2.6 % fewer
 // cycles at a 4 % lower clock, the same time; zeros for tokens are 17 % faster.
 // ---------------------------------------------------------------------------
-template <typename OT, bool DMA, int AHEAD, int WT, int WN, int FT, int FN>
+template <typename OT, bool DMA, bool NT, int AHEAD, int WT, int WN, int FT, int FN>
 __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, int tiles_t, int tiles_n)
 {
     constexpr int NW = WT * WN, BT = 32 * WT * FT, BN = 32 * WN * FN;
@@ -280,12 +289,12 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     auto fetch = [&](uint8_t *buf, int set) {            // sets out the next whole stage
 #pragma unroll
         for (int i = 0; i < CP; ++i) {
-            if constexpr (DMA)
-                __builtin_amdgcn_global_load_lds(
-                    (const __attribute__((address_space(1))) void *)src[i],
-                    (__attribute__((address_space(3))) void *)(buf + lds_at(i)), 16, 0, 0);
-            else
+            if constexpr (!DMA)
                 reg[set][i] = load16(src[i]);
+            else if (NT && i >= TP)
+                copy16<2>(src[i], buf + lds_at(i));
+            else
+                copy16<0>(src[i], buf + lds_at(i));
             src[i] += 128;
         }
     };
@@ -529,35 +538,46 @@ static void launch_stream(const LinArgs &a, hipStream_t st)
 }
 
 template <typename OT, bool DMA, int AHEAD, int WT, int WN, int FT, int FN>
-static void launch_tiles(const LinArgs &a, hipStream_t st)
+static void launch_tiles(const LinArgs &a, bool nt, hipStream_t st)
 {
     const int tt = (a.T + 32 * WT * FT - 1) / (32 * WT * FT), tn = (a.N + 32 * WN * FN - 1) / (32 * WN * FN);
     const unsigned grid = ((unsigned)tt * tn + 7) / 8 * 8;
-    launch(linear_tiles_kernel<OT, DMA, AHEAD, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
+    if (DMA && nt && tt == 1)                            // weights that nobody reads a second time
+        launch(linear_tiles_kernel<OT, DMA, DMA, AHEAD, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
+    else
+        launch(linear_tiles_kernel<OT, DMA, false, AHEAD, WT, WN, FT, FN>, grid, 64 * WT * WN, 0, st, a, tt, tn);
 }
 
 // ---------------------------------------------------------------------------
 // Choice of a kernel.  Times in us on an MI355X, launches in a row.
 //
-// Stream: up to 64 tokens, and more where its blocks still find a CU each
-// (256 x 512 x 6144: 6.4, tiles 12.0; 256 x 2048 x 7168: 11.3, 13.3; with one
-// and a half blocks per CU, 128 x 6144 x 6144, tiles win, 12.7 to 20.3).
+// Stream: up to 32 tokens, and more where its blocks still find a CU each
+// (256 x 512 x 6144: 6.4, tiles 12.0; 256 x 2048 x 7168: 11.3, 13.3; else tiles
+// win: 128 x 6144 x 6144 20.3, tiles 12.7; 64 x 12288 x 6144 20.8, 15.1;
+// 64 x 20000 x 512 11.4, 6.2).
 //  - Blocks are as small as leaves each a CU: 8 tokens, 16, 32 or 64, at most as
 //    many as there are, and 16, 32 or 48 weight rows (64 x 256 x 6144 in 16
 //    tokens x 16 rows 4.4, 32 x 16 5.2; 64 x 2048 x 7168 in 32 x 16 6.9, 64 x 16
 //    9.3; 171 x 896 x 5744 in 32 x 32 9.6, 64 x 32 13.7; 1748 x 192 x 8000 in
-//    32 x 48 14.3, 64 x 32 18.6; 32 x 8448 x 6144, 11.0, and in 32 x 32 14.8).
-//  - Up to 8 tokens 16 rows throughout (4 x 24576 x 6144: 22.8, with 32 rows
-//    23.4), in 16 waves where a CU has one block (1 x 512 x 12288: 5.5, with 8
+//    32 x 48 14.3, 64 x 32 18.6; 32 x 8448 x 6144, 11.0, and in 32 x 32 14.8);
+//    past that 32 rows by four waves, two blocks per CU (16 x 16000 x 5760:
+//    16.8, 48 x 8 waves 20.6, 16 x 8 18.7; 28 x 16080 x 4320 at odd strides
+//    17.7, 22.3, 23.4).
+//  - Up to 8 tokens 16 rows while 32 fit (4 x 8192 x 6144: 9.4, with 32 rows
+//    9.5), in 16 waves where a CU has one block (1 x 512 x 12288: 5.5, with 8
 //    waves 6.5; 8 x 2048 x 7168: 5.0, 5.4; 1 x 12288 x 2048, three blocks: 7.3,
 //    6.2).
-//  - 48 rows by four waves from 24576 channels on, two blocks per CU, where the
-//    tokens are read less often (24 x 24576 x 6144: 26.7, with 32 rows 28.1).
 //  - The non-temporal hint from 128 MiB of weights on, of which the 256 MiB
-//    last-level cache would not keep two (1 x 24576 x 6144: 23.2 with, 26.2
-//    without; 24: 26.7, 29.8).  Smaller weights may stay there from one call
-//    to the next and are read plainly: 32 x 6144 x 6144 8.9 from the cache, 12.1
-//    from memory; with the hint 11.7 from either.
+//    last-level cache would not keep two (1 x 24576 x 6144: 22.9 with, 26.5
+//    without; 24: 26.7, 29.8; tiles where a weight is read once, 128 x 24576 x
+//    6144: 40.2, 44.7).  Smaller weights may stay there from one call to the
+//    next and are read plainly: 32 x 6144 x 6144 8.9 from the cache, 12.1 from
+//    memory; with the hint 11.7 from either.  Rows that are not whole lines
+//    share lines, which the hint would fetch twice (24 x 12288 x 12288 at odd
+//    strides: 45.7 with, 42.3 without).  With it, up to 8 tokens 16 rows
+//    throughout (4 x 14336 x 8192: 21.9, 32 rows 28.7), for more 64 or 48 rows
+//    by four waves where 48 no longer fit (16 x 14336 x 8192: 64 rows 23.2, 48
+//    25.9; 24 x 24576 x 6144: 48 rows 26.7, 64 29; 32 rows 30).
 //
 // Tiles: a block's time is about its stages of 128 codes, each bound by what a
 // CU takes in (some 40 bytes a clock; 64 x 64 .. 192 x 128 tiles need 16 .. 40
@@ -589,29 +609,44 @@ static int64_t blocks_of(const LinArgs &a, int tokens, int rows)
     return (int64_t)((a.T + tokens - 1) / tokens) * ((a.N + rows - 1) / rows);
 }
 
+// weights worth the non-temporal hint: too large for the last-level cache to
+// keep from one call to the next, and their rows whole lines
+static bool passing(const LinArgs &a)
+{
+    return (int64_t)a.N * a.K > (128 << 20) && ops_aligned(a.w, 128) && a.ldw % 128 == 0;
+}
+
 template <typename OT, int TC>
 static void enqueue_stream(const LinArgs &a, hipStream_t st)
 {
-    const bool nt = (int64_t)a.N * a.K > (128 << 20);
-    const bool one = blocks_of(a, 8 * TC, 16) <= CUS;    // of the smallest blocks a CU each
+    const bool nt = passing(a);
+    auto fits = [&](int rows) { return blocks_of(a, 8 * TC, rows) <= CUS; };
     if constexpr (TC == 1) {
-        if (one)
+        if (fits(16))
             launch_stream<OT, false, 1, TC, 16>(a, st);
+        else if (nt)
+            launch_stream<OT, true, 1, TC, 8>(a, st);
+        else if (fits(32))
+            launch_stream<OT, false, 1, TC, 8>(a, st);
+        else if (fits(48))
+            launch_stream<OT, false, 3, TC, 8>(a, st);
         else
-            nt ? launch_stream<OT, true, 1, TC, 8>(a, st) : launch_stream<OT, false, 1, TC, 8>(a, st);
+            launch_stream<OT, false, 2, TC, 4>(a, st);
     } else if constexpr (TC == 8) {
         nt ? launch_stream<OT, true, 2, TC, 8>(a, st) : launch_stream<OT, false, 2, TC, 8>(a, st);
     } else {
-        if (one)
+        if (fits(16))
             launch_stream<OT, false, 1, TC, 8>(a, st);
-        else if (blocks_of(a, 8 * TC, 32) > CUS && blocks_of(a, 8 * TC, 48) <= CUS)
-            launch_stream<OT, false, 3, TC, 8>(a, st);
-        else if (nt && a.N >= 24576)
-            launch_stream<OT, true, 3, TC, 4>(a, st);
-        else if (nt)
-            launch_stream<OT, true, 2, TC, 8>(a, st);
+        else if (fits(32))
+            nt ? launch_stream<OT, true, 2, TC, 8>(a, st) : launch_stream<OT, false, 2, TC, 8>(a, st);
+        else if (fits(48))
+            nt ? launch_stream<OT, true, 3, TC, 8>(a, st) : launch_stream<OT, false, 3, TC, 8>(a, st);
+        else if (!nt)
+            launch_stream<OT, false, 2, TC, 4>(a, st);
+        else if (fits(64))
+            launch_stream<OT, true, 4, TC, 4>(a, st);
         else
-            launch_stream<OT, false, 2, TC, 8>(a, st);
+            launch_stream<OT, true, 3, TC, 4>(a, st);
     }
 }
 
@@ -640,15 +675,16 @@ static void enqueue_tiles(const LinArgs &a, hipStream_t st)
     }
     // copies: as many stages ahead as the LDS has room for, two blocks of the
     // smallest tiles to a CU; registers: as many as they hold
+    const bool nt = passing(a);
     switch (best) {
-    case 0: launch_tiles<OT, DMA, DMA ? 4 : 3, 2, 2, 1, 1>(a, st); break;
-    case 1: launch_tiles<OT, DMA, 3, 2, 2, 1, 2>(a, st); break;
-    case 2: launch_tiles<OT, DMA, 3, 1, 4, 3, 1>(a, st); break;
-    case 3: launch_tiles<OT, DMA, 3, 2, 2, 2, 2>(a, st); break;
-    case 4: launch_tiles<OT, DMA, 3, 2, 4, 3, 1>(a, st); break;
-    case 5: launch_tiles<OT, DMA, 3, 2, 4, 2, 2>(a, st); break;
-    case 6: launch_tiles<OT, DMA, 2, 2, 4, 3, 2>(a, st); break;
-    default: launch_tiles<OT, DMA, DMA ? 2 : 1, 2, 4, 4, 2>(a, st); break;
+    case 0: launch_tiles<OT, DMA, DMA ? 4 : 3, 2, 2, 1, 1>(a, nt, st); break;
+    case 1: launch_tiles<OT, DMA, 3, 2, 2, 1, 2>(a, nt, st); break;
+    case 2: launch_tiles<OT, DMA, 3, 1, 4, 3, 1>(a, nt, st); break;
+    case 3: launch_tiles<OT, DMA, 3, 2, 2, 2, 2>(a, nt, st); break;
+    case 4: launch_tiles<OT, DMA, 3, 2, 4, 3, 1>(a, nt, st); break;
+    case 5: launch_tiles<OT, DMA, 3, 2, 4, 2, 2>(a, nt, st); break;
+    case 6: launch_tiles<OT, DMA, 2, 2, 4, 3, 2>(a, nt, st); break;
+    default: launch_tiles<OT, DMA, DMA ? 2 : 1, 2, 4, 4, 2>(a, nt, st); break;
     }
 }
 
@@ -661,7 +697,7 @@ static void enqueue_linear(const LinArgs &a, hipStream_t st)
         enqueue_stream<OT, 2>(a, st);
     else if (a.T <= 32 || blocks_of(a, 32, 48) <= CUS)
         enqueue_stream<OT, 4>(a, st);
-    else if (a.T <= 64 || blocks_of(a, 64, 32) <= CUS)
+    else if (blocks_of(a, 64, 32) <= CUS)
         enqueue_stream<OT, 8>(a, st);
     else if (ops_aligned(a.q, 16) && ops_aligned(a.w, 16) && a.ldq % 16 == 0 && a.ldw % 16 == 0)
         enqueue_tiles<OT, true>(a, st);

@@ -300,9 +300,10 @@ def test_linear_tiles_at_every_count_of_stages(T, N, K, pad):
     check_linear(run_linear(q, s, w, ws, b, od, pad), q, s, w, ws, b, od)
 
 
-# weights split among 8 and 16 waves, in 16, 32 and 48 rows; tokens in 8, 16, 32
-# and 64, also more of them than one block takes
-@pytest.mark.parametrize("T,N,K", [(1, 4096, 1100), (8, 4100, 6100), (16, 9001, 1500), (32, 9001, 1500), (100, 300, 4500),
+# weights split among 4, 8 and 16 waves, in 16, 32 and 48 rows; tokens in 8, 16,
+# 32 and 64, also more of them than one block takes; and as tiles
+@pytest.mark.parametrize("T,N,K", [(5, 9001, 1100), (6, 13001, 1100), (13, 13001, 1100), (30, 13001, 1100), (33, 9001, 1100),
+                                   (1, 4096, 1100), (8, 4100, 6100), (16, 9001, 1500), (32, 9001, 1500), (100, 300, 4500),
                                    (70, 1999, 1500), (100, 2500, 1500), (500, 700, 1500), (210, 1900, 1500)])
 @pytest.mark.parametrize("pad", [0, 3])
 def test_linear_splits_of_a_weight_stream(T, N, K, pad):
@@ -322,6 +323,19 @@ def test_linear_few_tokens_many_channels(T, N, K, pad, shift):
 @pytest.mark.parametrize("T,N,K", [(3, 6200, 21700), (12, 6200, 21700), (12, 24600, 5505), (24, 6200, 21700),
                                    (24, 24577, 5504), (40, 6200, 21700), (40, 24577, 5504)])
 def test_linear_weights_beyond_the_cache(T, N, K):
+    check_large_weights(T, N, K)
+
+
+# rows of whole lines, whose weights pass the cache
+@pytest.mark.parametrize("T,N,K", [(8, 24600, 5504), (12, 6200, 21760), (14, 12200, 11136), (14, 16300, 8320),
+                                   (12, 24600, 5504), (30, 6200, 21760), (30, 12200, 11136), (30, 16300, 8320),
+                                   (32, 24577, 5504), (50, 6200, 21760), (60, 24577, 5504), (60, 8500, 15872),
+                                   (96, 24577, 5504), (128, 24577, 5504), (192, 24577, 5504), (250, 24577, 5504)])
+def test_linear_weights_of_whole_lines_beyond_the_cache(T, N, K):
+    check_large_weights(T, N, K)
+
+
+def check_large_weights(T, N, K):
     r = np.random.default_rng([7, T, N])
     q, w = r.integers(-128, 128, (T, K), dtype=np.int8), r.integers(-128, 128, (N, K), dtype=np.int8)
     s, ws = (0.01 + r.random(T)).astype(np.float32), (0.01 + r.random(N)).astype(np.float32)

@@ -206,7 +206,7 @@ __device__ __forceinline__ void copy16(const int8_t *from, uint8_t *to)
 // there); needs rows of 16-byte alignment.  Otherwise they pass through
 // registers.  The last, partial stage always does (load_codes gives its zeros).
 // 256 x 256 tiles of 4096 x 24576 x 6144: 531 us, 2330 TOP/s (the library's int8
-// product 575), the matrix units busy 61 % of the cycles at 1.78 GHz.  Bound by
+// product 575), the matrix units busy 63 % of the cycles at 1.78 GHz.  Bound by
 // power: copies one and a half stages ahead instead of one took 2.6 % fewer
 // cycles at a 4 % lower clock, the same time; zeros for tokens are 17 % faster.
 // ---------------------------------------------------------------------------

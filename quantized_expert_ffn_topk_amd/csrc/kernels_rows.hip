@@ -1,6 +1,18 @@
 // kernels_rows.hip -- row operators around the MoE layer on gfx950: the RMS
 // norm with the residual's addition, and SwiGLU, both with int8 output (codes
 // and one scale per row) beside or instead of bf16.
+//
+// A row needs its sum (norm) and its largest value before its first code: it is
+// read once, stays in the registers of 64 to 1024 threads, and is written from
+// there.  Bound by HBM from some hundred rows on, by the launch and a round trip
+// to memory below (kernel times under the profiler):
+//   norm   4096 x 6144, bf16, residual, codes    33.4 us, 176 MB at 5.3 TB/s (a
+//          333 x 7001, fp32, residual, codes      9.0      large copy runs at 4.9)
+//            1 x 6144, bf16, residual             2.4
+//   SwiGLU 4096 x 12288, bf16, codes             46.1, 252 MB at 5.5 TB/s
+//            1 x 12288                            3.8
+// SwiGLU's instructions alone are three quarters of its time: hence silu_mul's
+// form, the code by an addition and the maximum over two values at once.
 #include "ops_common.h"
 
 #include <cmath>
@@ -204,7 +216,9 @@ __device__ __forceinline__ bool row_of(int T, int *t, int *lane)
 }
 
 // RES: there is a residual.  All loads of the row and of gamma are issued
-// before any value is used.
+// before any value is used (waiting for one after the other 4096 x 6144 took
+// 44.5 us).  The sum is fp64: no fp32 row overflows it, and its order hardly ever
+// shows.
 template <int NT, int NV, typename XT, typename RT, bool RES>
 __global__ __launch_bounds__(block_threads<NT>()) void rmsnorm_kernel(NormArgs<XT, RT> a, RowOut o)
 {
@@ -320,8 +334,9 @@ __global__ __launch_bounds__(block_threads<NT>()) void swiglu_kernel(SwigluArgs<
 
 // ---------------------------------------------------------------------------
 // Rows too long for the registers (n > 32768), or shorter than a vector (n < 8):
-// value by value, a block reads the row again for each step; every value is read and written by one thread, the writes in
-// the last step, so h_out may be an input here too.
+// value by value, a block reads the row again for each step; every value is read
+// and written by one thread, the writes in the last step, so h_out may be an
+// input here too.
 // ---------------------------------------------------------------------------
 template <typename XT, typename RT>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs<XT, RT> a, RowOut o)
@@ -393,9 +408,20 @@ __global__ __launch_bounds__(1024) void swiglu_long_kernel(SwigluArgs<XT> a, Row
 }
 
 // ---------------------------------------------------------------------------
-// Shapes.  Many rows: few vectors are left idle and a block is small.  Few rows
-// (fewer than the 256 CUs): as many threads on a row as it has vectors, up to
-// 1024, since only the row's own latency counts.
+// Shapes: threads of a row x vectors of eight per thread, as few idle vectors as
+// there are, whatever the number of rows.  Fewer threads with more vectors wait
+// longer for each row, more threads meet later (us, launches in a graph, bf16 with
+// codes, norm / SwiGLU):
+//   4096 x  1024  128x1  6.4 /  6.1   64x2  6.6 /  6.1
+//   4096 x  2048  256x1 10.7 /  9.0  128x2 10.4 /  9.5   64x4 10.8 / 10.2
+//    100 x  2048  256x1  2.8 /  2.6  128x2  2.9 /  2.8   64x4  3.4 /  3.3
+//   4096 x  3000  256x2 14.6 / 13.9  128x3 14.9 / 12.7  512x1 15.5 / 13.7
+//   4096 x  4096  512x1 19.0 / 14.4  256x2 18.4 / 15.2
+//   4096 x  6144  256x3 27.9 / 22.6  512x2 28.2 / 24.1 1024x1 31.4 / 25.8
+//      1 x  6144  256x3  3.0 /  2.9  512x2  3.1 /  3.0 1024x1  3.1 /  3.0
+//   4096 x  8192  512x2 37.3 / 29.6  256x4 38.1 / 30.2 1024x1 42.5 / 30.1
+//   4096 x 12288  512x3 63.4 / 44.2 1024x2 78.7 / 47.2
+//   4096 x 16384  512x4 85.2 / 61.4 1024x2 94.0 / 59.0
 // ---------------------------------------------------------------------------
 constexpr int ROW_REG_MAX = 32768;
 
@@ -403,30 +429,22 @@ template <int V>
 using num = std::integral_constant<int, V>;
 
 template <typename F>
-static void with_shape(int n, int T, F &&f)
+static void with_shape(int n, F &&f)
 {
-    if (T < 256) {
-        if (n <= 512)
-            return f(num<64>(), num<1>());
-        if (n <= 2048)
-            return f(num<256>(), num<1>());
-        if (n <= 8192)
-            return f(num<1024>(), num<1>());
-        if (n <= 16384)
-            return f(num<1024>(), num<2>());
-    }
     if (n <= 512)
         return f(num<64>(), num<1>());
     if (n <= 1024)
-        return f(num<64>(), num<2>());
+        return f(num<128>(), num<1>());
     if (n <= 2048)
-        return f(num<64>(), num<4>());
-    if (n <= 4096)
+        return f(num<256>(), num<1>());
+    if (n <= 3328)
         return f(num<256>(), num<2>());
+    if (n <= 4096)
+        return f(num<512>(), num<1>());
     if (n <= 6144)
         return f(num<256>(), num<3>());
     if (n <= 8192)
-        return f(num<256>(), num<4>());
+        return f(num<512>(), num<2>());
     if (n <= 12288)
         return f(num<512>(), num<3>());
     if (n <= 16384)
@@ -448,7 +466,7 @@ static void enqueue_norm(const NormArgs<XT, RT> &a, const RowOut &o, hipStream_t
         launch(rmsnorm_long_kernel<XT, RT>, (unsigned)o.T, 1024, 0, st, a, o);
         return;
     }
-    with_shape(o.n, o.T, [&](auto nt, auto nv) {
+    with_shape(o.n, [&](auto nt, auto nv) {
         launch(rmsnorm_kernel<nt(), nv(), XT, RT, RES>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
     });
 }
@@ -460,7 +478,7 @@ static void enqueue_swiglu(const SwigluArgs<XT> &a, const RowOut &o, hipStream_t
         launch(swiglu_long_kernel<XT>, (unsigned)o.T, 1024, 0, st, a, o);
         return;
     }
-    with_shape(o.n, o.T, [&](auto nt, auto nv) {
+    with_shape(o.n, [&](auto nt, auto nv) {
         launch(swiglu_kernel<nt(), nv(), XT>, row_grid(o.T, nt()), block_threads<nt()>(), 0, st, a, o);
     });
 }

@@ -109,6 +109,14 @@ def test_norm_widths(H, xd, rd):
     check_norm(run_norm(x, res, gamma, xd, rd), x, res, gamma, rd)
 
 
+# on both sides of each length at which a row gets other threads
+@pytest.mark.parametrize("H", [1024, 1025, 3328, 3329, 4096, 4097, 6145, 12288, 12289, 16384, 24576, 24577])
+@pytest.mark.parametrize("xd,rd", [("bf16", "bf16"), ("f32", "f32")])
+def test_norm_widths_between_shapes(H, xd, rd):
+    x, res, gamma = norm_inputs(2, 5, H, xd, rd)
+    check_norm(run_norm(x, res, gamma, xd, rd), x, res, gamma, rd)
+
+
 @pytest.mark.parametrize("T", [1, 3, 4, 257])
 @pytest.mark.parametrize("xd,rd", [("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 1)])
@@ -199,6 +207,12 @@ def test_swiglu(dt, T, F, pad, shift):
     v = ref.swiglu(gu)
     check_bf16(y, v, SWIGLU_TOL)
     ref.check_codes(q, s, v, SWIGLU_TOL)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("F", [512, 1024, 1025, 3328, 3329, 4096, 4097, 6145, 8192, 8193, 12289, 16385, 24577])
+def test_swiglu_widths_between_shapes(dt, F):
+    test_swiglu(dt, 5, F, 3, 1)
 
 
 @pytest.mark.parametrize("F", [40, 33003])

@@ -4,7 +4,9 @@ Argument marshalling only: every step of the layer runs in the library's HIP
 kernels.  Device buffers may be given as torch tensors (their data_ptr() is
 passed), as integers (raw addresses) or as None (NULL).  Streams are torch
 streams, raw hipStream_t integers or None (the null stream).  A non-OK status
-raises MoEError carrying moe_last_error().
+raises MoEError carrying moe_last_error().  The operators around the layer are
+called through _calls, a module of their own: on one token their kernels take
+as long as ctypes takes for their arguments.
 """
 import ctypes as C
 import os
@@ -250,26 +252,40 @@ def moe_layer_forward_noalloc(desc, x, T, weights, idx_out, gate_w_out, out, str
                                           stream_handle(stream)))
 
 
+_calls = None
+
+
+def calls():
+    """The module of direct calls, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise RuntimeError("_calls.so is not built "
+                               "(python -m quantized_expert_ffn_topk_amd.build)") from e
+        m.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in m.NAMES), check, addr)
+        _calls = m
+    return _calls
+
+
 def moe_rmsnorm_quant(x, x_dtype, ldx, residual, res_dtype, ldr, gamma, T, H, eps, h_out, ldh,
                       y_out, ldy, q, ldq, s, stream=None):
-    check(lib().moe_rmsnorm_quant(addr(x), x_dtype, ldx, addr(residual), res_dtype, ldr, addr(gamma),
-                                  T, H, eps, addr(h_out), ldh, addr(y_out), ldy, addr(q), ldq,
-                                  addr(s), stream_handle(stream)))
+    (_calls or calls()).moe_rmsnorm_quant(x, x_dtype, ldx, residual, res_dtype, ldr, gamma, T, H, eps,
+                                          h_out, ldh, y_out, ldy, q, ldq, s, stream)
 
 
 def moe_swiglu_quant(gu, gu_dtype, ld, T, F, y_out, ldy, q, ldq, s, stream=None):
-    check(lib().moe_swiglu_quant(addr(gu), gu_dtype, ld, T, F, addr(y_out), ldy, addr(q), ldq,
-                                 addr(s), stream_handle(stream)))
+    (_calls or calls()).moe_swiglu_quant(gu, gu_dtype, ld, T, F, y_out, ldy, q, ldq, s, stream)
 
 
 def moe_linear_int8(q, ldq, s, T, w, ldw, ws, bias, N, K, out, out_dtype, ldo, stream=None):
-    check(lib().moe_linear_int8(addr(q), ldq, addr(s), T, addr(w), ldw, addr(ws), addr(bias), N, K,
-                                addr(out), out_dtype, ldo, stream_handle(stream)))
+    (_calls or calls()).moe_linear_int8(q, ldq, s, T, w, ldw, ws, bias, N, K, out, out_dtype, ldo, stream)
 
 
 def moe_route_select(desc, logits, logit_dtype, ld, bias, T, idx, gate_w, stream=None):
-    check(lib().moe_route_select(C.byref(desc), addr(logits), logit_dtype, ld, addr(bias), T,
-                                 addr(idx), addr(gate_w), stream_handle(stream)))
+    (_calls or calls()).moe_route_select(desc, logits, logit_dtype, ld, bias, T, idx, gate_w, stream)
 
 
 def moe_router_topk_grouped(ctx, desc, x, T, weights, idx, gate_w, stream=None):

@@ -1,22 +1,26 @@
-"""Builds libmoe.so (HIP kernels for gfx950 + the C ABI) in-tree.
+"""Builds libmoe.so (HIP kernels for gfx950 + the C ABI) and _calls.so (direct
+calls of the operators from Python) in-tree.
 
     python -m quantized_expert_ffn_topk_amd.build
 
-Objects go to _build/ at the repository root; the library lands next to this
-file.  Kernels are compiled with fp contraction off and packed-fp32 code
+Objects go to _build/ at the repository root; the libraries land next to
+this file.  Kernels are compiled with fp contraction off and packed-fp32 code
 generation disabled.
 """
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+CALLS = os.path.join(PKG, "_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 HIP_SOURCES = ["kernels_router.hip", "kernels_gemv.hip", "kernels_bs1.hip", "kernels_gemm.hip",
                "kernels_mx.hip", "noalloc.hip", "kernels_probe.hip", "kernels_rows.hip",
@@ -43,6 +47,16 @@ def _compile(src):
     return obj, "\n".join(lines)
 
 
+def _link(cmd, lib, verbose):
+    tmp = lib + ".tmp"
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, lib)
+    if verbose:
+        print("built", lib, flush=True)
+
+
 def build(verbose=True, jobs=None):
     os.makedirs(BUILD, exist_ok=True)
     sources = HIP_SOURCES + CPP_SOURCES
@@ -52,14 +66,9 @@ def build(verbose=True, jobs=None):
     for (obj, msg), src in zip(results, sources):
         if verbose and msg:
             print("[%s]\n%s" % (src, msg), flush=True)
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
-    os.replace(tmp, LIB)
-    if verbose:
-        print("built", LIB, flush=True)
+    _link([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950"] + [o for o, _ in results], LIB, verbose)
+    _link([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + os.path.join(ROOT, "include"),
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "pycalls.cpp")], CALLS, verbose)
     return LIB
 
 

@@ -116,3 +116,40 @@ def test_reference_select_worked_values():
     np.testing.assert_allclose(w, [2 * s])
     idx, w, _ = ref.select(l, np.array([0, 0, 0, 0, 0, 9.0]), 1, True, 1, 1, 1, True, 1.0)
     assert idx.tolist() == [[5]] and w.tolist() == [[1.0]]
+
+
+# ---- the direct calls' own conversions ---------------------------------------------
+def test_direct_calls_take_numpy_arrays_and_integers():
+    gu, q, s = np.zeros((0, 16), np.float32), np.zeros((0, 8), np.int8), np.zeros(0, np.float32)
+    abi.moe_swiglu_quant(gu, abi.DT_F32, np.int64(16), 0, np.int32(8), None, 8, q, 8, s)
+    abi.moe_swiglu_quant(P, abi.DT_F32, 16, 0, 8, None, 8, P, 8, P, stream=0)
+
+
+@pytest.mark.parametrize("bad,error", [
+    (dict(gu="x"), TypeError), (dict(gu=1.5), TypeError), (dict(gu=object()), TypeError),
+    (dict(T="2"), TypeError), (dict(T=2.0), TypeError), (dict(T=None), TypeError),
+    (dict(T=1 << 31), OverflowError), (dict(F=-(1 << 31) - 1), OverflowError), (dict(ld=1 << 63), OverflowError),
+    (dict(stream="s"), AttributeError), (dict(stream=1.0), AttributeError)])
+def test_direct_calls_refuse_what_they_cannot_convert(bad, error):
+    with pytest.raises(error):
+        abi.moe_swiglu_quant(**{**SWIGLU, **bad})
+    # and nothing of it is left behind
+    refused(lambda: abi.moe_swiglu_quant(**{**SWIGLU, "T": -1}))
+
+
+def test_direct_calls_take_a_tensor_whose_address_fails_as_that_error():
+    class Tensor:
+        def data_ptr(self):
+            raise RuntimeError("no storage")
+
+    with pytest.raises(RuntimeError, match="no storage"):
+        abi.moe_swiglu_quant(**{**SWIGLU, "gu": Tensor()})
+
+
+def test_direct_calls_need_the_whole_description():
+    with pytest.raises(TypeError):
+        abi.moe_route_select(abi.moe_cache_event(), P, 0, 8, None, 1, P, P)
+    with pytest.raises(TypeError):
+        abi.moe_route_select(None, P, 0, 8, None, 1, P, P)
+    with pytest.raises(TypeError):
+        abi.calls().moe_linear_int8(P, 1)

@@ -567,17 +567,19 @@ static void launch_tiles(const LinArgs &a, bool nt, hipStream_t st)
 //    9.5), in 16 waves where a CU has one block (1 x 512 x 12288: 5.5, with 8
 //    waves 6.5; 8 x 2048 x 7168: 5.0, 5.4; 1 x 12288 x 2048, three blocks: 7.3,
 //    6.2).
-//  - The non-temporal hint from 128 MiB of weights on, of which the 256 MiB
-//    last-level cache would not keep two (1 x 24576 x 6144: 22.9 with, 26.5
-//    without; 24: 26.7, 29.8; tiles where a weight is read once, 128 x 24576 x
-//    6144: 40.2, 44.7).  Smaller weights may stay there from one call to the
-//    next and are read plainly: 32 x 6144 x 6144 8.9 from the cache, 12.1 from
-//    memory; with the hint 11.7 from either.  Rows that are not whole lines
-//    share lines, which the hint would fetch twice (24 x 12288 x 12288 at odd
-//    strides: 45.7 with, 42.3 without).  With it, up to 8 tokens 16 rows
-//    throughout (4 x 14336 x 8192: 21.9, 32 rows 28.7), for more 64 or 48 rows
-//    by four waves where 48 no longer fit (16 x 14336 x 8192: 64 rows 23.2, 48
-//    25.9; 24 x 24576 x 6144: 48 rows 26.7, 64 29; 32 rows 30).
+//  - The non-temporal hint from 96 MiB of weights on, of which the 256 MiB
+//    last-level cache keeps hardly two (3 x 24576 x 4480: 17.7 with, 19.5
+//    without; 24 x 24576 x 6144: 26.7, 29.8; tiles where a weight is read once,
+//    128 x 24576 x 6144: 40.2, 44.7; at 91 MiB, 24 x 13312 x 7168 from three
+//    sets of weights in turn: 20.1, 19.5).  Smaller weights may stay there from
+//    one call to the next and are read plainly: 32 x 6144 x 6144 8.9 from the
+//    cache, 12.1 from memory; with the hint 11.7 from either.  Rows that are not
+//    whole lines share lines, which the hint would fetch twice (24 x 12288 x
+//    12288 at odd strides: 45.7 with, 42.3 without).  With it, 64 rows by four
+//    waves where 48 no longer fit (16 x 14336 x 8192: 64 rows 23.2, 48 25.9;
+//    3 x 14336 x 8192: 22.4, 32 rows 28.7), past that 48 rows (24 x 24576 x
+//    6144: 26.7, 64 rows 29, 32 rows 30), up to 8 tokens 32 (3 x 24576 x 4480:
+//    17.7, 48 rows 18.0, 16 rows of eight waves 19.8).
 //
 // Tiles: a block's time is about its stages of 128 codes, each bound by what a
 // CU takes in (some 40 bytes a clock; 64 x 64 .. 192 x 128 tiles need 16 .. 40
@@ -613,7 +615,7 @@ static int64_t blocks_of(const LinArgs &a, int tokens, int rows)
 // keep from one call to the next, and their rows whole lines
 static bool passing(const LinArgs &a)
 {
-    return (int64_t)a.N * a.K > (128 << 20) && ops_aligned(a.w, 128) && a.ldw % 128 == 0;
+    return (int64_t)a.N * a.K >= (96 << 20) && ops_aligned(a.w, 128) && a.ldw % 128 == 0;
 }
 
 template <typename OT, int TC>
@@ -624,14 +626,14 @@ static void enqueue_stream(const LinArgs &a, hipStream_t st)
     if constexpr (TC == 1) {
         if (fits(16))
             launch_stream<OT, false, 1, TC, 16>(a, st);
-        else if (nt)
-            launch_stream<OT, true, 1, TC, 8>(a, st);
         else if (fits(32))
-            launch_stream<OT, false, 1, TC, 8>(a, st);
+            nt ? launch_stream<OT, true, 1, TC, 8>(a, st) : launch_stream<OT, false, 1, TC, 8>(a, st);
         else if (fits(48))
-            launch_stream<OT, false, 3, TC, 8>(a, st);
+            nt ? launch_stream<OT, true, 3, TC, 8>(a, st) : launch_stream<OT, false, 3, TC, 8>(a, st);
+        else if (nt && fits(64))
+            launch_stream<OT, true, 4, TC, 4>(a, st);
         else
-            launch_stream<OT, false, 2, TC, 4>(a, st);
+            nt ? launch_stream<OT, true, 2, TC, 4>(a, st) : launch_stream<OT, false, 2, TC, 4>(a, st);
     } else if constexpr (TC == 8) {
         nt ? launch_stream<OT, true, 2, TC, 8>(a, st) : launch_stream<OT, false, 2, TC, 8>(a, st);
     } else {

@@ -341,7 +341,7 @@ def test_linear_weights_beyond_the_cache(T, N, K):
 
 
 # rows of whole lines, whose weights pass the cache
-@pytest.mark.parametrize("T,N,K", [(8, 24600, 5504), (12, 6200, 21760), (14, 12200, 11136), (14, 16300, 8320),
+@pytest.mark.parametrize("T,N,K", [(8, 24600, 5504), (7, 6200, 21760), (5, 12200, 11136), (2, 16300, 8320), (12, 6200, 21760), (14, 12200, 11136), (14, 16300, 8320),
                                    (12, 24600, 5504), (30, 6200, 21760), (30, 12200, 11136), (30, 16300, 8320),
                                    (32, 24577, 5504), (50, 6200, 21760), (60, 24577, 5504), (60, 8500, 15872),
                                    (96, 24577, 5504), (128, 24577, 5504), (192, 24577, 5504), (250, 24577, 5504)])

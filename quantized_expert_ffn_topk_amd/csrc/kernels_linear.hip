@@ -47,15 +47,6 @@ __device__ __forceinline__ v4i load_codes(const int8_t *row, int k, int K)
     return v;
 }
 
-template <typename OT>
-__device__ __forceinline__ void store_out(const LinArgs &a, int t, int n, int acc)
-{
-    float y = ((float)acc * a.s[t]) * a.ws[n];
-    if (a.bias)
-        y += a.bias[n];
-    store1(static_cast<OT *>(a.out) + (int64_t)t * a.ldo + n, y);
-}
-
 // ---------------------------------------------------------------------------
 // Few tokens: a stream of weights.  A block owns 16*RT weight rows and up to
 // 8*TC tokens; its W waves take stages of 128 codes of K in turn (so that a
@@ -106,6 +97,23 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
         put[u] = 128 * (lane >> 3) + 16 * ((lane & 7) ^ (4 * u + (lane >> 4)));
         at[u] = 128 * (lane & 15) + 16 * ((4 * u + (lane >> 4)) ^ ((lane >> 1) & 7));
     }
+    // the scales of the outputs that this thread will write, on their way from the
+    // beginning (read at the end, cold, they cost 1 x 6144 x 6144 7.8 us instead of
+    // 7.35, 16 x 4096 x 4096 7.2 instead of 6.7)
+    constexpr int IT = (RT * TB + W - 1) / W;
+    float s[IT], ws[IT][4], bias[IT][4];
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int f = min((int)threadIdx.x + 64 * W * it, RT * TB * 64 - 1), l = f & 63, ij = f >> 6;
+        s[it] = a.s[min(t0 + 16 * (ij % TB) + (l & 15), a.T - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = min(n0 + 16 * (ij / TB) + 4 * (l >> 4) + i, a.N - 1);
+            ws[it][i] = a.ws[n];
+            bias[it][i] = a.bias ? a.bias[n] : 0.0f;
+        }
+    }
+    asm volatile("" ::: "memory");
     v4i acc[RT][TB], reg[CP], wv[2][RT], qv[2][TB];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -169,8 +177,11 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
         for (int j = 0; j < TB; ++j)
             part[(i * TB + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    for (int f = threadIdx.x; f < RT * TB * 64; f += 64 * W) {
-        const int l = f & 63, ij = f >> 6;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int f = (int)threadIdx.x + 64 * W * it, l = f & 63, ij = f >> 6;
+        if (f >= RT * TB * 64)
+            break;
         v4i sum = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < W; ++w)
@@ -178,9 +189,13 @@ __global__ __launch_bounds__(64 * W) void linear_stream_kernel(LinArgs a)
         const int n = n0 + 16 * (ij / TB) + 4 * (l >> 4), c = 16 * (ij % TB) + (l & 15), t = t0 + c;
         if (c < 8 * TC && t < a.T) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                float y = ((float)sum[i] * s[it]) * ws[it][i];
+                if (a.bias)
+                    y += bias[it][i];
                 if (n + i < a.N)
-                    store_out<OT>(a, t, n + i, sum[i]);
+                    store1(static_cast<OT *>(a.out) + (int64_t)t * a.ldo + n + i, y);
+            }
         }
     }
 }
@@ -226,6 +241,7 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     __shared__ __align__(128) uint8_t buf1[BUF];
     __shared__ __align__(128) uint8_t buf2[NB > 2 ? BUF : 16];
     __shared__ __align__(128) uint8_t buf3[NB > 3 ? BUF : 16];
+    __shared__ __align__(16) float scale[BT + 2 * BN];   // tokens' scales, channels', biases
 
     // tiles in groups of 8 token tiles, token tile fastest, each XCD (blocks
     // with the same index mod 8) a contiguous run of them
@@ -249,6 +265,21 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     }
     auto lds_at = [&](int i) { return (i < TP ? 0 : BT * 128) + 1024 * (wave + NW * (i < TP ? i : i - TP)); };
 
+    // the epilogue's scales go to LDS ahead of all rows, 64 at a time (read at the
+    // end, cold, they cost 333 x 5003 x 2048 10.1 us instead of 9.55, 1500 x 2048 x
+    // 2048 12.7 instead of 11.5)
+    auto bring = [&](const float *from, int first, int count, float *to, int at) {
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)(from + min(first + at + lane, count - 1)),
+            (__attribute__((address_space(3))) void *)(to + at), 4, 0, 0);
+    };
+    for (int i = wave; 64 * i < BT; i += NW)
+        bring(a.s, t0, a.T, scale, min(64 * i, BT - 64));
+    for (int i = wave; 64 * i < BN; i += NW) {
+        bring(a.ws, n0, a.N, scale + BT, 64 * i);
+        if (a.bias)
+            bring(a.bias, n0, a.N, scale + BT + BN, 64 * i);
+    }
     v16i acc[FT][FN];
 #pragma unroll
     for (int i = 0; i < FT; ++i)
@@ -472,24 +503,26 @@ __global__ __launch_bounds__(64 * WT * WN) void linear_tiles_kernel(LinArgs a, i
     constexpr int VE = 16 / (int)sizeof(OT);             // values per lane
     static_assert(32 * PITCH * NW / 2 <= BUF, "half of the waves' parts fit one buffer");
     const int nw0 = n0 + 32 * FN * wn, tw0 = t0 + 32 * FT * wt;
-    if (tail)
-        __syncthreads();                                 // buf0 has been read
     uint8_t *mine = (wave < NW / 2 ? buf0 : buf1) + (wave % (NW / 2)) * 32 * PITCH;
+    // every wave's scales are there, and its reads of buf0 done
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);                  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     float ws[FN][16], bias[FN][16];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int n = nw0 + 32 * j + 8 * g + 4 * (lane >> 5);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ws[j][4 * g + e] = a.ws[min(n + e, a.N - 1)];
-                bias[j][4 * g + e] = a.bias ? a.bias[min(n + e, a.N - 1)] : 0.0f;
-            }
+            const float *at = scale + BT + 32 * (FN * wn + j) + 8 * g + 4 * (lane >> 5);
+            const float4 w = *reinterpret_cast<const float4 *>(at);
+            const float4 b = *reinterpret_cast<const float4 *>(at + BN);   // not used unless there is a bias
+            ws[j][4 * g] = w.x, ws[j][4 * g + 1] = w.y, ws[j][4 * g + 2] = w.z, ws[j][4 * g + 3] = w.w;
+            bias[j][4 * g] = b.x, bias[j][4 * g + 1] = b.y, bias[j][4 * g + 2] = b.z, bias[j][4 * g + 3] = b.w;
         }
 #pragma unroll
     for (int i = 0; i < FT; ++i) {
-        const float st = a.s[min(tw0 + 32 * i + (lane & 31), a.T - 1)];
+        const float st = scale[32 * (FT * wt + i) + (lane & 31)];
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll

@@ -286,8 +286,9 @@ moe_status moe_linear_int8(const int8_t *q, int64_t ldq, const float *s, int32_t
  *  n_experts E in [1, 1024], top_k k in [1, 32], n_group in [1, 64] a divisor of
  *  E, topk_group in [1, n_group], k <= topk_group * E/n_group, group_best 1 or 2
  *  (2 only with at least 2 experts a group), renorm 0 or 1, scale finite and >= 0.
- * moe_route_select: from logits of MOE_DT_F32 or MOE_DT_BF16, scores in fp32;
- * bias [E] fp32 or NULL.  No context.
+ * moe_route_select: from logits of MOE_DT_F32 or MOE_DT_BF16, scores in fp32 (its
+ * subnormals included: below 2^-150 a score is 0); bias [E] fp32 or NULL.  No
+ * context.
  * moe_router_topk_grouped: moe_router_topk with this choice instead of its own:
  * x [T,H] bf16 and w->router_w give the fp64 logits (the kernels and the
  * workspace of ctx), w->router_bias the bias (NULL for none), scores in fp64.  desc's n_experts must

@@ -78,15 +78,16 @@ __device__ __forceinline__ double wave_sum(double v)
 // exp and reciprocal.  fp32: 2^(v*log2 e) with the product's remainder added, so
 // that the error does not grow with |v|, and the hardware's reciprocal, each
 // about a unit in the last place (the library's exp and an IEEE quotient were a
-// fifth of the selection's instructions); fp64: the library's.
-__device__ __forceinline__ float exp_of(float v)
+// fifth of the selection's instructions); v up to 88, 0 past -200 (for -inf too).
+// fp64: the library's.
+__device__ __forceinline__ float exp_of(float v, float above = 0.0f)
 {
     const float L2E = 1.44269502f, L2E_LO = 1.92596303e-8f;   // log2(e) = L2E + L2E_LO
-    const float t = v * L2E;
-    const float r = fmaf(v, L2E, -t) + v * L2E_LO;
-    const float e = __builtin_amdgcn_exp2f(t);
-    // past 2^126 (and for -inf) 0 or infinity as it is
-    return (fabsf(t) < 126.0f) ? fmaf(e, r * 0.693147181f, e) : e;
+    const float a = __builtin_amdgcn_fmed3f(v, -200.0f, 88.0f);
+    const float t = a * L2E;
+    const float r = fmaf(a, L2E, -t) + a * L2E_LO;
+    const float e = __builtin_amdgcn_exp2f(t + above);
+    return fmaf(e, r * 0.693147181f, e);
 }
 __device__ __forceinline__ double exp_of(double v)
 {
@@ -99,6 +100,66 @@ __device__ __forceinline__ float inverse(float v)
 __device__ __forceinline__ double inverse(double v)
 {
     return 1.0 / v;
+}
+
+// The hardware's 2^t and reciprocal give 0 below 2^-126.  Scores there (v from
+// -200 to -80; 0 from -104 on) keep their order as fp32's subnormals: 2^t is taken
+// 2^64 higher and brought down by an exact product that rounds once.  Rarely
+// needed, so a wave asks once for all its values.
+__device__ __forceinline__ bool is_low(float v)
+{
+    return fabsf(v + 140.0f) < 60.0f;
+}
+__device__ __forceinline__ float exp_low(float v)
+{
+    return exp_of(v, 64.0f) * 0x1p-64f;
+}
+
+// p[j] = exp(v[j]), v[j] <= 0
+template <int NE>
+__device__ __forceinline__ void exp_each(const float (&v)[NE], float (&p)[NE])
+{
+    bool low = false;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        p[j] = exp_of(v[j]);
+        low |= is_low(v[j]);
+    }
+    if (__ballot(low)) {
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            p[j] = is_low(v[j]) ? exp_low(v[j]) : p[j];
+    }
+}
+template <int NE>
+__device__ __forceinline__ void exp_each(const double (&v)[NE], double (&p)[NE])
+{
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+        p[j] = exp_of(v[j]);
+}
+// p[j] = 1/(1 + exp(-l[j])), which is exp(l[j]) in fp32 where that is low
+template <int NE>
+__device__ __forceinline__ void sigmoid_each(const float (&l)[NE], float (&p)[NE])
+{
+    bool low = false;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        p[j] = inverse(1.0f + exp_of(-l[j]));
+        low |= is_low(l[j]);
+    }
+    if (__ballot(low)) {
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            p[j] = is_low(l[j]) ? exp_low(l[j]) : p[j];
+    }
+}
+template <int NE>
+__device__ __forceinline__ void sigmoid_each(const double (&l)[NE], double (&p)[NE])
+{
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+        p[j] = inverse(1.0 + exp_of(-l[j]));
 }
 
 // A candidate: its key and its expert, in the order of choice: the larger key,
@@ -282,10 +343,14 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
             m = (l[j] > m) ? l[j] : m;                  // a NaN is never larger
         const Key mk = wave_top(order_key(m));
         m = lane_value(m, __builtin_ctzll(__ballot(order_key(m) == mk)));
-        S sum = 0;
+        S sum = 0, v[NE];
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            v[j] = l[j] - m;
+        exp_each(v, p);
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-            const S e = (m == inf) ? (l[j] == inf ? (S)1 : (S)0) : exp_of(l[j] - m);
+            const S e = (m == inf) ? (l[j] == inf ? (S)1 : (S)0) : p[j];
             p[j] = (l[j] > -inf) ? e : (S)0;            // 0 for -inf and NaN, whatever m is
             sum += p[j];
         }
@@ -295,9 +360,10 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
         for (int j = 0; j < NE; ++j)
             p[j] *= by;
     } else {
+        sigmoid_each(l, p);
 #pragma unroll
         for (int j = 0; j < NE; ++j)
-            p[j] = (l[j] == l[j]) ? inverse((S)1 + exp_of(-l[j])) : (S)0;
+            p[j] = (l[j] == l[j]) ? p[j] : (S)0;
     }
 #pragma unroll
     for (int j = 0; j < NE; ++j) {

@@ -42,13 +42,18 @@ def _rows(t, name, width, dtypes=None):
 
 def quantise_weight(w):
     """int8 codes [N, K] and fp32 channel scales [N] of a weight matrix: the rule
-    of the activations, per output channel (a zero channel gets scale 0)."""
+    of the activations, per output channel.  A zero channel gets scale 0; one with
+    a NaN or an infinity gets scale NaN and codes 0; one below 2^-96 is multiplied
+    by 2^64 first (exact), so that 127/max stays finite."""
     import torch
     w = w.float()
     amax = w.abs().amax(dim=1)
-    inv = torch.where(amax > 0, 127.0 / amax, torch.zeros_like(amax))
-    q = torch.clamp(torch.round(w * inv[:, None]), -127, 127).to(torch.int8)
-    return q.contiguous(), amax / 127.0
+    fine = torch.isfinite(amax)
+    pre = torch.ones_like(amax).masked_fill(amax < 2.0 ** -96, 2.0 ** 64)
+    inv = torch.where(fine & (amax > 0), 127.0 / (amax * pre), 0.0)
+    q = torch.clamp(torch.round((w * pre[:, None]) * inv[:, None]), -127, 127)
+    q = torch.where(fine[:, None], q, 0.0).to(torch.int8)
+    return q.contiguous(), torch.where(fine, amax / 127.0, float("nan"))
 
 
 class _Norm:

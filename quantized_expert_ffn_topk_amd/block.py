@@ -63,6 +63,8 @@ class _Norm:
         import torch
         if gamma.dim() != 1:
             raise ValueError("gamma must be a vector")
+        if gamma.device.type != "cuda":
+            raise ValueError("gamma is on %s, not on a GPU" % gamma.device)
         self.torch = torch
         self.gamma = gamma.float().contiguous()
         self.H = gamma.shape[0]
@@ -91,6 +93,8 @@ class _Norm:
             return t.cuda.stream(t.cuda.default_stream(self.dev))
         if isinstance(stream, int):
             return t.cuda.stream(t.cuda.ExternalStream(stream, device=self.dev))
+        if stream.device != self.dev:
+            raise ValueError("the stream is of %s, not of %s" % (stream.device, self.dev))
         return t.cuda.stream(stream)
 
     def _norm(self, x, residual, y, q, s, stream):
@@ -150,6 +154,8 @@ class MoEFFN(_Norm):
 
     def __init__(self, gamma, layer, route, eps=1e-6):
         super().__init__(gamma, layer.max_tokens, eps)
+        if layer.dev != self.dev:
+            raise ValueError("the layer is on %s, gamma on %s" % (layer.dev, self.dev))
         if layer.desc.hidden != self.H:
             raise ValueError("the layer's hidden is %d, gamma has %d" % (layer.desc.hidden, self.H))
         if route.top_k != layer.desc.top_k or route.n_experts != layer.desc.n_experts:

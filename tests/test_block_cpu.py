@@ -47,3 +47,30 @@ def test_quantise_weight_marks_a_channel_that_is_not_finite(bad):
     q, s = quantise_weight(w)
     assert q[1].tolist() == [0] * 5 and torch.isnan(s[1])
     assert (q[[0, 2]] == 127).all() and not torch.isnan(s[[0, 2]]).any()
+
+
+# ---------------------------------------------------------------------------
+# everything of a half is on one GPU: a host address, or another GPU's, never reaches a kernel
+# ---------------------------------------------------------------------------
+def dense_parts(device, H=16, F=8):
+    z = lambda *shape: torch.zeros(shape, dtype=torch.int8, device=device)  # noqa: E731
+    o = lambda n: torch.ones(n, device=device)  # noqa: E731
+    return o(H), z(2 * F, H), o(2 * F), z(H, F), o(H)
+
+
+def layer_like(dev, H=16):
+    from types import SimpleNamespace
+    return SimpleNamespace(desc=SimpleNamespace(hidden=H, top_k=2, n_experts=8), dev=dev, max_tokens=4)
+
+
+def route():
+    from quantized_expert_ffn_topk_amd import abi
+    return abi.moe_route_desc(8, 2, abi.SCORE_SIGMOID, 1, 1, 1, 1, 1.0)
+
+
+def test_halves_refuse_host_tensors():
+    from quantized_expert_ffn_topk_amd.block import DenseFFN, MoEFFN
+    with pytest.raises(ValueError, match="GPU"):
+        DenseFFN(*dense_parts("cpu"), max_tokens=4)
+    with pytest.raises(ValueError, match="GPU"):
+        MoEFFN(torch.ones(16), layer_like(torch.device("cuda", 0)), route())

@@ -85,20 +85,38 @@ class _Norm:
             raise ValueError("x and residual must be on %s" % self.dev)
         return T, ldx, ldr
 
-    def _on(self, stream):
-        """The device, and torch's current stream: what is allocated inside belongs
-        to the stream that writes it."""
+    def _made(self):
+        """The end of a constructor.  The object's rows and weights lie where earlier
+        work of torch's current stream may still be at work, and may themselves be
+        on their way: it is waited for, so that forward may use any stream."""
         t = self.torch
-        if stream is None:
-            return t.cuda.stream(t.cuda.default_stream(self.dev))
+        home = t.cuda.current_stream(self.dev)
+        home.synchronize()
+        self._known = {home}
+        self._own = [a for a in vars(self).values() if isinstance(a, t.Tensor)]
+
+    def _on(self, stream, x, residual):
+        """The device, and torch's current stream: what is allocated inside belongs
+        to the stream that writes it.  The object's tensors and the inputs are
+        recorded on a stream that is not their own, so that dropping them early does
+        not give their memory away under the kernels."""
+        t = self.torch
         if isinstance(stream, int):
             return t.cuda.stream(t.cuda.ExternalStream(stream, device=self.dev))
-        if stream.device != self.dev:
-            raise ValueError("the stream is of %s, not of %s" % (stream.device, self.dev))
-        return t.cuda.stream(stream)
+        s = t.cuda.default_stream(self.dev) if stream is None else stream
+        if s.device != self.dev:
+            raise ValueError("the stream is of %s, not of %s" % (s.device, self.dev))
+        if s not in self._known:
+            for a in self._own:
+                a.record_stream(s)
+            self._known.add(s)
+        if s != t.cuda.current_stream(self.dev):
+            x.record_stream(s)
+            residual.record_stream(s)
+        return t.cuda.stream(s)
 
-    def _norm(self, x, residual, y, q, s, stream):
-        T, ldx, ldr = self._check(x, residual)
+    def _norm(self, x, residual, rows, y, q, s, stream):
+        T, ldx, ldr = rows
         h = self.torch.empty((T, self.H), dtype=residual.dtype, device=self.dev)
         abi.moe_rmsnorm_quant(x, _dtype(x), ldx, residual, _dtype(residual), ldr, self.gamma, T, self.H,
                               self.eps, h, self.H, y, self.H, q, self.H, s, stream)
@@ -130,14 +148,20 @@ class DenseFFN(_Norm):
         self.q, self.s = e(n, H, dt=t.int8), e(n, dt=t.float32)
         self.gu = e(n, 2 * F, dt=t.bfloat16)
         self.qh, self.sh = e(n, F, dt=t.int8), e(n, dt=t.float32)
+        self._made()
 
     def forward(self, x, residual, stream=None):
         """(output [T, H], new residual [T, H]); enqueued on `stream` (None: the
         null stream), which the inputs must be ready on and the outputs belong
-        to.  One call at a time: the intermediate rows are the object's own."""
+        to: whoever reads them on another stream waits for this one, and records
+        them there before dropping them.  One call at a time: the intermediate
+        rows are the object's own, so a call on another stream has to wait for the
+        last one.  A raw handle of a stream says nothing about how long it lives:
+        with one, the inputs and the object are kept until its work is done."""
         H, F = self.H, self.F
-        with self._on(stream):
-            T, h = self._norm(x, residual, None, self.q, self.s, stream)
+        rows = self._check(x, residual)
+        with self._on(stream, x, residual):
+            T, h = self._norm(x, residual, rows, None, self.q, self.s, stream)
             out = self.torch.empty((T, H), dtype=self.out_dtype, device=self.dev)
             abi.moe_linear_int8(self.q, H, self.s, T, self.gate_up, H, self.s_gu, None, 2 * F, H, self.gu,
                                 abi.DT_BF16, 2 * F, stream)
@@ -165,13 +189,15 @@ class MoEFFN(_Norm):
         self.y = t.empty((self.max_tokens, self.H), dtype=t.bfloat16, device=self.dev)
         self.idx = t.empty((self.max_tokens, route.top_k), dtype=t.int32, device=self.dev)
         self.w = t.empty((self.max_tokens, route.top_k), dtype=t.float32, device=self.dev)
+        self._made()
 
     def forward(self, x, residual, stream=None):
         """As DenseFFN.forward; the chosen experts and their weights are in
         idx[:T] and w[:T] afterwards."""
         odt = self.torch.bfloat16 if self.layer.desc.out_dtype == abi.DT_BF16 else self.torch.float32
-        with self._on(stream):
-            T, h = self._norm(x, residual, self.y, None, None, stream)
+        rows = self._check(x, residual)
+        with self._on(stream, x, residual):
+            T, h = self._norm(x, residual, rows, self.y, None, None, stream)
             out = self.torch.empty((T, self.H), dtype=odt, device=self.dev)
             abi.moe_router_topk_grouped(self.layer.ctx, self.route, self.y, T, self.layer.weights, self.idx,
                                         self.w, stream)

@@ -130,6 +130,8 @@ class DenseFFN(_Norm):
     def __init__(self, gamma, gate_up, s_gu, down, s_dn, max_tokens, eps=1e-6, out_dtype=None):
         super().__init__(gamma, max_tokens, eps)
         t, H = self.torch, self.H
+        if gate_up.dim() != 2 or down.dim() != 2:
+            raise ValueError("gate_up and down must be matrices")
         F = down.shape[1]
         if gate_up.dtype != t.int8 or down.dtype != t.int8:
             raise ValueError("weights must be int8 codes")
@@ -143,6 +145,8 @@ class DenseFFN(_Norm):
         if any(a.device != self.dev for a in (self.gate_up, self.down, self.s_gu, self.s_dn)):
             raise ValueError("weights and gamma must be on one device")
         self.out_dtype = out_dtype or t.bfloat16
+        if self.out_dtype not in (t.float32, t.bfloat16):
+            raise ValueError("out_dtype must be fp32 or bf16, not %s" % self.out_dtype)
         n = self.max_tokens
         e = lambda *shape, dt: t.empty(shape, dtype=dt, device=self.dev)  # noqa: E731
         self.q, self.s = e(n, H, dt=t.int8), e(n, dt=t.float32)

@@ -25,6 +25,18 @@ def test_halves_refuse_a_stream_of_another_gpu():
         d.forward(x, x, other)
 
 
+def test_dense_half_refuses_bad_weights_and_types_when_it_is_made():
+    from quantized_expert_ffn_topk_amd.block import DenseFFN
+    gamma, gu, s_gu, dn, s_dn = dense_parts("cuda")
+    for bad in (dict(out_dtype=torch.float16), dict(out_dtype=torch.int8)):
+        with pytest.raises(ValueError, match="out_dtype"):
+            DenseFFN(gamma, gu, s_gu, dn, s_dn, 4, **bad)
+    for parts in ((gamma, gu, s_gu, dn[0], s_dn), (gamma, gu.flatten(), s_gu, dn, s_dn)):
+        with pytest.raises(ValueError):
+            DenseFFN(*parts, 4)
+    assert DenseFFN(gamma, gu, s_gu, dn, s_dn, 4, out_dtype=torch.float32).out_dtype == torch.float32
+
+
 # ---------------------------------------------------------------------------
 # tensors and streams
 # ---------------------------------------------------------------------------

@@ -5,16 +5,20 @@ kernels.  Device buffers may be given as torch tensors (their data_ptr() is
 passed), as integers (raw addresses) or as None (NULL).  Streams are torch
 streams, raw hipStream_t integers or None (the null stream).  A non-OK status
 raises MoEError carrying moe_last_error().  The operators around the layer are
-called through _calls, a module of their own: on one token their kernels take
-as long as ctypes takes for their arguments.
+called through _calls, a module of their own (on one token their kernels take
+as long as ctypes takes for their arguments), and through ctypes where that
+module is not built.
 """
 import ctypes as C
+import operator
 import os
+import types
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # MOE_LIB: another build of the same library (an instrumented host build, an
 # A/B variant); the in-tree libmoe.so otherwise
 LIB_PATH = os.environ.get("MOE_LIB") or os.path.join(PKG, "libmoe.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe.h")
 
 OK, E_INVAL, E_UNSUPPORTED, E_NOMEM, E_HIP, E_CAPACITY = range(6)
@@ -255,17 +259,49 @@ def moe_layer_forward_noalloc(desc, x, T, weights, idx_out, gate_w_out, out, str
 _calls = None
 
 
+def _whole(bits):
+    """A whole number of so many bits, refused as the direct calls do (ctypes would
+    drop what is above)."""
+    def convert(x):
+        x = operator.index(x)
+        if not -(1 << (bits - 1)) <= x < 1 << (bits - 1):
+            raise OverflowError("%d does not fit %d bits" % (x, bits))
+        return x
+    return convert
+
+
+def _route(d):
+    if not isinstance(d, moe_route_desc):
+        raise TypeError("a moe_route_desc is wanted, not %r" % type(d))
+    return C.byref(d)
+
+
+def _through_ctypes(name):
+    """The direct call `name` without the module: its arguments and its errors."""
+    kinds = {C.c_void_p: addr, C.c_int32: _whole(32), C.c_int64: _whole(64), C.c_float: C.c_float,
+             C.POINTER(moe_route_desc): _route}
+    f = getattr(lib(), name)
+    converts = [kinds[k] for k in f.argtypes[:-1]] + [stream_handle]
+
+    def call(*args):
+        if len(args) != len(converts):
+            raise TypeError("%d arguments, %d wanted" % (len(args), len(converts)))
+        check(f(*[c(a) for c, a in zip(converts, args)]))
+    return call
+
+
 def calls():
-    """The module of direct calls, bound to the loaded library."""
+    """The module of direct calls, bound to the loaded library; where it has not
+    been built, the same calls through ctypes."""
     global _calls
     if _calls is None:
         L = lib()
-        try:
+        if os.path.exists(CALLS_PATH):
             from . import _calls as m
-        except ImportError as e:
-            raise RuntimeError("_calls.so is not built "
-                               "(python -m quantized_expert_ffn_topk_amd.build)") from e
-        m.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in m.NAMES), check, addr)
+            m.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in m.NAMES), check, addr)
+        else:
+            m = types.SimpleNamespace(**{n: _through_ctypes(n) for n in (
+                "moe_rmsnorm_quant", "moe_swiglu_quant", "moe_linear_int8", "moe_route_select")})
         _calls = m
     return _calls
 

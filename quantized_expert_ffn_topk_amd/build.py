@@ -5,10 +5,12 @@ calls of the operators from Python) in-tree.
 
 Objects go to _build/ at the repository root; the libraries land next to
 this file.  Kernels are compiled with fp contraction off and packed-fp32 code
-generation disabled.
+generation disabled.  _calls.so is left out where there is no Python.h or no
+C++ compiler for it; those calls then go through ctypes.
 """
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -57,6 +59,22 @@ def _link(cmd, lib, verbose):
         print("built", lib, flush=True)
 
 
+def build_calls(verbose=True):
+    """Builds _calls.so; its path, or None where it cannot be built (then there is
+    no file of an earlier build either)."""
+    include = sysconfig.get_paths()["include"]
+    missing = [what for what, there in (("Python.h in " + include, os.path.exists(os.path.join(include, "Python.h"))),
+                                        (CXX, shutil.which(CXX.split()[0]))) if not there]
+    if missing:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        print("without %s: no _calls.so, the operators are called through ctypes" % " and ".join(missing), flush=True)
+        return None
+    _link(CXX.split() + ["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + os.path.join(ROOT, "include"),
+                         "-I" + include, os.path.join(CSRC, "pycalls.cpp")], CALLS, verbose)
+    return CALLS
+
+
 def build(verbose=True, jobs=None):
     os.makedirs(BUILD, exist_ok=True)
     sources = HIP_SOURCES + CPP_SOURCES
@@ -67,8 +85,7 @@ def build(verbose=True, jobs=None):
         if verbose and msg:
             print("[%s]\n%s" % (src, msg), flush=True)
     _link([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950"] + [o for o, _ in results], LIB, verbose)
-    _link([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + os.path.join(ROOT, "include"),
-           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "pycalls.cpp")], CALLS, verbose)
+    build_calls(verbose)
     return LIB
 
 

@@ -14,6 +14,8 @@ import operator
 import os
 import types
 
+import numpy as np
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 # MOE_LIB: another build of the same library (an instrumented host build, an
 # A/B variant); the in-tree libmoe.so otherwise
@@ -157,12 +159,16 @@ def exported_names():
 # ---------------------------------------------------------------------------
 def addr(x):
     """Device/host address of a tensor, numpy array, int or None."""
-    if x is None:
-        return None
+    kind = type(x)
+    if x is None or kind is int:
+        return x
+    if kind is np.ndarray:
+        return x.ctypes.data
     try:
-        return x.data_ptr()                     # the common case, without asking first
+        return x.data_ptr()                     # a tensor, without asking first
     except AttributeError:
-        pass
+        if hasattr(x, "data_ptr"):              # its own error
+            raise
     if isinstance(x, int):
         return x
     if hasattr(x, "ctypes"):

@@ -74,3 +74,34 @@ def test_build_goes_on_without_the_module(without, monkeypatch, tmp_path, capsys
 def test_build_makes_the_module_where_it_can(monkeypatch, tmp_path):
     monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
     assert build.build_calls(verbose=False) == build.CALLS and os.path.getsize(build.CALLS) > 0
+
+
+class Failing:
+    def data_ptr(self):
+        raise AttributeError("storage is gone")
+
+
+def test_addresses():
+    class Flag(int):
+        pass
+
+    class Pointer:
+        def data_ptr(self):
+            return 77
+
+    a = np.arange(4)
+    assert [abi.addr(x) for x in (None, 5, True, Flag(9), Pointer(), a)] == [None, 5, 1, 9, 77, a.ctypes.data]
+    assert abi.addr(a[2:]) == a.ctypes.data + 16
+    for x in ("x", 1.5, object()):
+        with pytest.raises(TypeError):
+            abi.addr(x)
+
+
+def test_an_error_inside_data_ptr_is_passed_on():
+    with pytest.raises(AttributeError, match="storage is gone"):
+        abi.addr(Failing())
+
+
+def test_an_error_inside_data_ptr_is_passed_on_by_the_direct_calls():
+    with pytest.raises(AttributeError, match="storage is gone"):
+        abi.moe_swiglu_quant(**{**t.SWIGLU, "gu": Failing()})

@@ -1,6 +1,6 @@
 """GPU tests of every kernel that the int8 product's choice can take, in both output types: each shape
 first has to be one that takes the kernel it stands for, so that a change of the choice cannot
-quietly leave one untested.
+quietly leave one untested.  Likewise the two ways of the layer's router logits.
 
 The product's bits are defined (exact sum, fp32 epilogue in a fixed order), so there is no tolerance."""
 import numpy as np
@@ -156,3 +156,45 @@ def test_the_shapes_reach_every_kernel_of_the_choice():
     ways = {(w, h) for w, h in (("copies", False), ("copies", True), ("registers", False))}
     assert {k for k, _ in TILES} == {(w, h, t[0], t[1]) for w, h in ways for t in rule.tiles()}
     assert len({k for k, _ in STREAMS}) == 26
+
+
+# ---------------------------------------------------------------------------
+# grouped selection behind logits that two launches' halves make: the selection adds them and keeps
+# the sum
+# ---------------------------------------------------------------------------
+def logit_parts(T, H, E):
+    """How many parts of H the router's logits come in, as kernels_router.hip's router_ksplit states it."""
+    if T <= 16 or T >= 1024 or -(-E // 16) * -(-T // 16) >= 128:
+        return 1
+    h32 = H // 32
+    return 2 if h32 % (16 if h32 % 16 else 32) == 0 else 1
+
+
+@pytest.mark.parametrize("T,H,E,parts", [(17, 1024, 64, 2), (40, 2048, 100, 2), (100, 1024, 250, 2), (33, 6144, 48, 2),
+                                         (16, 1024, 64, 1), (120, 1024, 256, 1), (40, 1280, 100, 1)])
+def test_grouped_router_adds_both_halves_of_the_logits(T, H, E, parts):
+    from quantized_expert_ffn_topk_amd import synth
+    from tests import operators_ref as ref
+    from tests.gpu_common import Case
+    from tests.test_gpu_operators import U
+    assert logit_parts(T, H, E) == parts
+    k = 6
+    c = Case(13, T, H, 256, E, k, 0, r=2.5, n_distinct=1)
+    lay = c.layer(max_tokens=T)
+    x = lay.x_tensor(c.x)
+    logits = synth.bf16_bits_to_f32(c.x).astype(np.float64) @ c.Wr.astype(np.float64).T
+    idx, w = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    G = next(g for g in (8, 5, 4, 2) if E % g == 0)
+    for softmax, best, renorm, bias in ((False, 2, True, True), (True, 1, False, True), (False, 1, True, False)):
+        d = abi.moe_route_desc(E, k, int(softmax), G, max(1, G // 2), best, int(renorm), 1.5)
+        weights = lay.weights if bias else abi.moe_layer_weights(lay.weights.router_w, None, lay.weights.expert_ptrs, None)
+        abi.moe_router_topk_grouped(lay.ctx, d, x, T, weights, idx, w)
+        torch.cuda.synchronize()
+        want, ww, margin = ref.select(logits, c.b if bias else None, k, softmax, G, max(1, G // 2), best, renorm, 1.5)
+        assert margin > 1e-12
+        assert np.array_equal(idx.cpu().numpy(), want)
+        np.testing.assert_allclose(w.cpu().numpy(), ww, rtol=2 * U)
+        # the whole logits can be read afterwards
+        got = lay.debug_read(2, (T, E), torch.float64).cpu().numpy()
+        np.testing.assert_allclose(got, logits, rtol=1e-11, atol=1e-11)
+    lay.close()

@@ -88,3 +88,46 @@ def test_select_scores_below_the_smallest_number_are_zero(softmax):
     first = [31, 0, 1, 2] if softmax else [0, 1, 2, 3]
     assert idx.tolist() == [first] * 3
     assert w.tolist() == ([[2.5, 0, 0, 0]] * 3 if softmax else [[0.0] * 4] * 3)
+
+
+# ---------------------------------------------------------------------------
+# bf16 outputs at both ends of the range: rounded to nearest even, no tolerance where the fp32 value's
+# bits are defined
+# ---------------------------------------------------------------------------
+def same_bits(got, want):
+    """bf16 values held as fp32: equal bits, any NaN for a NaN."""
+    got, want = got.astype(np.float32), want.astype(np.float32)
+    nan = np.isnan(want)
+    assert np.isnan(got[nan]).all()
+    assert np.array_equal(got[~nan].view(np.uint32), want[~nan].view(np.uint32)), \
+        list(zip(got[got != want][:4], want[got != want][:4]))
+
+
+@pytest.mark.parametrize("T,N,K", [(6, 40, 100), (70, 4200, 48)])
+def test_linear_bf16_subnormal_and_overflowing_outputs(T, N, K):
+    from tests.test_gpu_operators import lin_inputs, run_linear
+    q, s, w, ws, _ = lin_inputs(31, T, N, K)
+    s[0::5] *= np.float32(1e-24)                         # y from 1e-42 to 1e-37
+    s[1::5] *= np.float32(1e16)                          # y past fp32's largest number, and just below it
+    s[2::5], s[4::5] = np.float32(np.inf), np.float32(np.nan)
+    ws = (ws * np.float32(1e-18)).astype(np.float32)
+    ws[1::3] *= np.float32(1e36)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = ref.linear(q, s, w, ws, None)
+        same_bits(run_linear(q, s, w, ws, None, "bf16"), ref.bf16(want))
+    got = run_linear(q, s, w, ws, None, "f32")
+    nan = np.isnan(want)
+    assert np.isnan(got[nan]).all() and np.array_equal(got[~nan].view(np.uint32), want[~nan].view(np.uint32))
+    assert ((np.abs(want) < 2.0 ** -126) & (want != 0)).any() and np.isinf(want).any() and nan.any()
+
+
+@pytest.mark.parametrize("H", [6, 300, 6144, 33001])
+def test_norm_new_residual_of_subnormal_sums(H):
+    from tests.test_gpu_operators import run_norm
+    r = np.random.default_rng([32, H])
+    x = (r.standard_normal((3, H)) * 1e-39).astype(np.float32)
+    res = ref.bf16(r.standard_normal((3, H)) * 1e-39)
+    res[1], x[2] = 0.0, -res[2]                          # sums that are subnormal, and exact zeros
+    h = run_norm(x, res, None, "f32", "bf16")[0]
+    same_bits(h, ref.bf16(x + res))
+    assert np.array_equal(run_norm(x, res, None, "f32", "f32")[0], x + res)

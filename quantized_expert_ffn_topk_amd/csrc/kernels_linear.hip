@@ -582,9 +582,9 @@ static void launch_tiles(const LinArgs &a, bool nt, hipStream_t st)
 }
 
 // ---------------------------------------------------------------------------
-// Choice of a kernel.  Times in us on an MI355X, launches in a row, taken with
-// the outputs' scales still read at the end; now they are 0.3 to 1.2 less for all
-// kernels alike (24 x 24576 x 6144: 26.1, 128 x 6144 x 6144 12.2).
+// Choice of a kernel.  Times in us on an MI355X, launches in a row.  Those of the
+// streams were taken with the outputs' scales still read at the end; now they are
+// 0.3 to 1.2 less for all of them alike (24 x 24576 x 6144: 26.1).
 //
 // Stream: up to 32 tokens, and more where its blocks still find a CU each
 // (256 x 512 x 6144: 6.4, tiles 12.0; 256 x 2048 x 7168: 11.3, 13.3; else tiles
@@ -621,20 +621,24 @@ static void launch_tiles(const LinArgs &a, bool nt, hipStream_t st)
 // KiB a stage) or by its products (256 x 256), and a fixed part, the first
 // stage's way and the output.  Blocks go to 256 CUs in rounds; two of the
 // smallest tiles fit a CU and share their fixed parts, and one that is alone
-// takes longer per stage.  The tile whose rounds take least is taken.  The times
-// are fitted to 139 shapes of 65 to 4096 tokens, 64 to 12288 long: the tile
-// taken is on average 0.2 % slower than the fastest of the eight, at most 8 %.
-// (With 64x64, 64x128, 128x128, 128x256 and 256x256 alone the fastest are 4.5 %
-// slower.)  64x64 / 64x128 / 96x128 / 128x128 / 192x128 / 128x256 / 192x256 /
-// 256x256:
-//    128 x  6144 x 6144   12.7 / 18.5 / 22.0 / 25.1 / 29.9 / 36.9 / 48.4 / 60.8
-//    256 x 12288 x 6144   30.9 / 31.6 / 45.0 / 28.1 / 33.6 / 38.0 / 49.5 / 61.7
-//    451 x  4992 x 2688   16.0 / 15.4 / 14.3 / 14.8 / 17.3 / 20.2 / 26.6 / 33.7
-//    520 x  9856 x 3008   39.2 / 35.2 / 34.0 / 36.3 / 24.8 / 27.6 / 35.5 / 40.3
-//    600 x  8192 x 4096   33.5 / 34.2 / 34.1 / 38.4 / 27.7 / 28.5 / 36.0 / 44.5
-//   1309 x  7360 x 1344   37.2 / 30.8 / 38.8 / 34.8 / 25.8 / 31.3 / 21.6 / 26.1
-//   2048 x 24576 x 2048    217 /  173 /  192 /  176 /  145 /  131 /  128 /  106
-//   3000 x  8000 x 8000    361 /  294 /  311 /  252 /  232 /  206 /  203 /  213
+// takes longer per stage.  The tile whose rounds cost least is taken.  The costs
+// rank the tiles and are no times: they were fitted to 139 shapes of 65 to 4096
+// tokens, 64 to 12288 long, for the loss against the fastest tile, and a cost is
+// 0.5 to 1.6 times the measured time (the median 0.97, of the tile taken 0.85;
+// 128 x 6144 x 6144 as 64 x 64: cost 18.0, 12.2 us).  The tile taken is 0.3 %
+// slower than the fastest of the eight on average, at most 8 %, on those shapes
+// as on 100 others drawn afterwards; profiles/int8_product_tiles.csv has all
+// times, and a test holds the costs below to them.  (With 64x64, 64x128, 128x128,
+// 128x256 and 256x256 alone the fastest are 2.7 % slower.)  64x64 / 64x128 /
+// 96x128 / 128x128 / 192x128 / 128x256 / 192x256 / 256x256:
+//    128 x  6144 x 6144   12.2 / 17.6 / 20.7 / 23.8 / 29.0 / 35.9 / 47.8 / 60.3
+//    256 x 12288 x 6144   31.8 / 30.9 / 42.8 / 27.9 / 33.6 / 36.0 / 48.9 / 62.0
+//    451 x  4992 x 2688   15.5 / 15.2 / 12.4 / 13.5 / 16.0 / 19.6 / 26.0 / 33.0
+//    520 x  9856 x 3008   36.5 / 33.5 / 34.2 / 36.0 / 26.1 / 28.6 / 37.5 / 39.6
+//    600 x  8192 x 4096   36.4 / 33.8 / 33.0 / 36.5 / 29.3 / 28.8 / 35.0 / 44.4
+//   1309 x  7360 x 1344   34.8 / 29.3 / 36.1 / 33.1 / 26.2 / 30.0 / 21.5 / 25.0
+//   2048 x 24576 x 2048    218 /  173 /  186 /  171 /  143 /  135 /  132 /  110
+//   3000 x  8000 x 8000    376 /  309 /  317 /  260 /  239 /  215 /  207 /  219
 // Rows that are not 16-byte aligned pass through registers: each piece crosses a
 // line (a quarter more time), and at odd addresses another quarter (128 x 6144 x
 // 6144: 12.7 aligned, 24 at odd strides; 4096 x 24576 x 6144: 535, 770).
@@ -692,7 +696,7 @@ static void enqueue_tiles(const LinArgs &a, hipStream_t st)
 {
     struct Tile {
         int bt, bn, fit;                                 // blocks of it that fit a CU
-        double stage, fixed, alone;                      // us, see above
+        double stage, fixed, alone;                      // costs, see above
     };
     static constexpr Tile tile[8] = {
         {64, 64, 2, 0.211, 2.4, 0.113},  {64, 128, 2, 0.313, 3.4, 0.079}, {96, 128, 1, 0.548, 3.8, 0.0},
@@ -704,10 +708,10 @@ static void enqueue_tiles(const LinArgs &a, hipStream_t st)
         const Tile &t = tile[i];
         const int64_t n = (blocks_of(a, t.bt, t.bn) + CUS - 1) / CUS;
         const double k = a.K / 128.0, alone = n % t.fit ? t.alone : 0.0;
-        const double us = (n * t.stage + alone) * k + (n + t.fit - 1) / t.fit * t.fixed;
-        if (i == 0 || us < least) {
+        const double cost = (n * t.stage + alone) * k + (n + t.fit - 1) / t.fit * t.fixed;
+        if (i == 0 || cost < least) {
             best = i;
-            least = us;
+            least = cost;
         }
     }
     // copies: as many stages ahead as the LDS has room for, two blocks of the

@@ -408,20 +408,32 @@ __global__ __launch_bounds__(1024) void swiglu_long_kernel(SwigluArgs<XT> a, Row
 }
 
 // ---------------------------------------------------------------------------
-// Shapes: threads of a row x vectors of eight per thread, as few idle vectors as
-// there are, whatever the number of rows.  Fewer threads with more vectors wait
-// longer for each row, more threads meet later (us, launches in a graph, bf16 with
-// codes, norm / SwiGLU):
+// Shapes: threads of a row x vectors of eight per thread, one rule by the row's
+// length for both operators and any number of rows.  Fewer threads with more
+// vectors wait longer for each row, more threads meet later, idle vectors cost
+// their instructions (us, launches in a graph, bf16 with codes, norm / SwiGLU):
 //   4096 x  1024  128x1  6.4 /  6.1   64x2  6.6 /  6.1
 //   4096 x  2048  256x1 10.7 /  9.0  128x2 10.4 /  9.5   64x4 10.8 / 10.2
 //    100 x  2048  256x1  2.8 /  2.6  128x2  2.9 /  2.8   64x4  3.4 /  3.3
-//   4096 x  3000  256x2 14.6 / 13.9  128x3 14.9 / 12.7  512x1 15.5 / 13.7
-//   4096 x  4096  512x1 19.0 / 14.4  256x2 18.4 / 15.2
-//   4096 x  6144  256x3 27.9 / 22.6  512x2 28.2 / 24.1 1024x1 31.4 / 25.8
-//      1 x  6144  256x3  3.0 /  2.9  512x2  3.1 /  3.0 1024x1  3.1 /  3.0
-//   4096 x  8192  512x2 37.3 / 29.6  256x4 38.1 / 30.2 1024x1 42.5 / 30.1
-//   4096 x 12288  512x3 63.4 / 44.2 1024x2 78.7 / 47.2
-//   4096 x 16384  512x4 85.2 / 61.4 1024x2 94.0 / 59.0
+//      1 x  2560  256x2  2.7 /  2.5  128x3  2.9 /  2.8  512x1  2.6 /  2.4
+//    100 x  2560  256x2  3.1 /  2.9  128x3  3.3 /  3.1  512x1  3.0 /  2.8
+//   1000 x  2560  256x2  5.4 /  5.2  128x3  5.3 /  4.7  512x1  5.6 /  5.2
+//   4096 x  2560  256x2 12.7 / 12.9  128x3 12.8 / 11.4  512x1 13.9 / 12.7
+//   4096 x  3328  256x2 15.6 / 13.9                     512x1 16.1 / 13.7
+//      1 x  4096  512x1  2.6 /  2.4  256x2  2.7 /  2.5
+//   4096 x  4096  512x1 19.0 / 14.3  256x2 18.4 / 14.9
+//   4096 x  6144  256x3 30.2 / 23.1  512x2 30.2 / 24.2 1024x1 34.3 / 27.2
+//      1 x  6144  256x3  3.0 /  2.8  512x2  3.0 /  3.0 1024x1  3.0 /  2.9
+//   4096 x  8192  512x2 38.3 / 29.4  256x4 38.7 / 30.3 1024x1 43.9 / 30.3
+//      1 x  8192  512x2  3.1 /  3.0  256x4  3.4 /  3.2 1024x1  3.2 /  3.1
+//   4096 x 12288  512x3 64.4 / 44.1 1024x2 79.9 / 47.1
+//   4096 x 16384  512x4 85.5 / 61.4 1024x2 94.9 / 58.9
+// From 2049 to 4096 no shape is best throughout: 512x1 is 0.1 us faster than
+// 256x2 on up to 100 rows, and slower on thousands of the norm's, by 11 % at 2056
+// and less and less from there; it is taken from where that is below 4 %.  128x3,
+// with the fewest idle vectors, is 10 % faster for thousands of SwiGLU's rows, 10
+// to 12 % slower for a few, and holds three quarters as many values.  At 16384 the norm
+// would lose more with 1024x2 than SwiGLU gains.
 // ---------------------------------------------------------------------------
 constexpr int ROW_REG_MAX = 32768;
 

@@ -221,10 +221,12 @@ moe_status moe_layer_forward_noalloc(const moe_layer_desc *desc, const void *x, 
  * What a block needs next to its MoE layer: the norm in front of it, the dense
  * FFN of the blocks without experts ("Guide Complet de Colibri", table "Points
  * techniques cles", router row: the first three layers are dense), and routing
- * with groups.  These calls take no context: they only enqueue kernels on
- * `stream` of the current device, allocate nothing, keep nothing from one call
- * to the next and need no workspace; any number may run at once on different
- * streams.  They may be captured into a HIP graph.
+ * with groups.  These calls (but for moe_router_topk_grouped, which is the
+ * layer's router: its context's workspace, device and one call at a time) take no
+ * context: they only enqueue kernels on `stream` of the current device, allocate
+ * nothing, keep nothing from one call to the next and need no workspace; any
+ * number may run at once on different streams.  They may be captured into a HIP
+ * graph.
  * A leading dimension ld is the distance between rows in elements (at least the
  * row's length); pointers need only their element's alignment.  T is in
  * [0, 2^20]; T == 0 does nothing.  Inputs and outputs must not overlap except

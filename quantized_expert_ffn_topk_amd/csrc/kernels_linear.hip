@@ -608,7 +608,11 @@ static void launch_tiles(const LinArgs &a, bool nt, hipStream_t st)
 //    128 x 24576 x 6144: 40.2, 44.7; at 91 MiB, 24 x 13312 x 7168 from three
 //    sets of weights in turn: 20.1, 19.5).  Smaller weights may stay there from
 //    one call to the next and are read plainly: 32 x 6144 x 6144 8.9 from the
-//    cache, 12.1 from memory; with the hint 11.7 from either.  Rows that are not
+//    cache, 12.1 from memory; with the hint 11.7 from either.  Where other layers
+//    pass the cache between two calls they come from memory: one set of weights
+//    again and again / 750 MB of them in turn, 1 x 6144 x 6144 6.9 / 9.1, 24 x 6144
+//    x 6144 7.7 / 12.6, 8 x 12288 x 6144 12.9 / 15.8, 128 x 6144 x 6144 (tiles)
+//    12.2 / 19.1, 1 x 2048 x 7168 3.8 / 6.1.  Rows that are not
 //    whole lines share lines, which the hint would fetch twice (24 x 12288 x
 //    12288 at odd strides: 45.7 with, 42.3 without).  With it, 64 rows by four
 //    waves where 48 no longer fit (16 x 14336 x 8192: 64 rows 23.2, 48 25.9;
@@ -641,7 +645,7 @@ static void launch_tiles(const LinArgs &a, bool nt, hipStream_t st)
 //   3000 x  8000 x 8000    376 /  309 /  317 /  260 /  239 /  215 /  207 /  219
 // Rows that are not 16-byte aligned pass through registers: each piece crosses a
 // line (a quarter more time), and at odd addresses another quarter (128 x 6144 x
-// 6144: 12.7 aligned, 24 at odd strides; 4096 x 24576 x 6144: 535, 770).
+// 6144: 12.3 aligned, 23.5 at odd strides; 4096 x 24576 x 6144: 529, 768).
 // ---------------------------------------------------------------------------
 constexpr int64_t CUS = 256;
 

@@ -7,9 +7,9 @@
 // there.  Bound by HBM from some hundred rows on, by the launch and a round trip
 // to memory below (kernel times under the profiler):
 //   norm   4096 x 6144, bf16, residual, codes    33.8 us, 176 MB at 5.3 TB/s (a
-//          333 x 7001, fp32, residual, codes      7.2      large copy runs at 4.9)
+//          333 x 7001, fp32, residual, codes    7 to 8     large copy runs at 4.9)
 //            1 x 6144, bf16, residual             2.3
-//   SwiGLU 4096 x 12288, bf16, codes             46.3, 252 MB at 5.4 TB/s
+//   SwiGLU 4096 x 12288, bf16, codes         46 to 48, 252 MB at 5.2 to 5.4 TB/s
 //            1 x 12288                            3.4
 // SwiGLU's instructions alone are three quarters of its time: hence silu_mul's
 // form, the code by an addition and the maximum over two values at once.

@@ -138,7 +138,8 @@ __device__ __forceinline__ void exp_each(const double (&v)[NE], double (&p)[NE])
     for (int j = 0; j < NE; ++j)
         p[j] = exp_of(v[j]);
 }
-// p[j] = 1/(1 + exp(-l[j])), which is exp(l[j]) in fp32 where that is low
+// p[j] = 1/(1 + exp(-l[j])), which is exp(l[j]) in fp32 where that is low, and 0
+// below (for -inf too); 0 for a NaN
 template <int NE>
 __device__ __forceinline__ void sigmoid_each(const float (&l)[NE], float (&p)[NE])
 {
@@ -146,6 +147,7 @@ __device__ __forceinline__ void sigmoid_each(const float (&l)[NE], float (&p)[NE
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
         p[j] = inverse(1.0f + exp_of(-l[j]));
+        p[j] = (l[j] > -200.0f) ? p[j] : 0.0f;
         low |= is_low(l[j]);
     }
     if (__ballot(low)) {
@@ -158,8 +160,10 @@ template <int NE>
 __device__ __forceinline__ void sigmoid_each(const double (&l)[NE], double (&p)[NE])
 {
 #pragma unroll
-    for (int j = 0; j < NE; ++j)
+    for (int j = 0; j < NE; ++j) {
         p[j] = inverse(1.0 + exp_of(-l[j]));
+        p[j] = (l[j] == l[j]) ? p[j] : 0.0;
+    }
 }
 
 // A candidate: its key and its expert, in the order of choice: the larger key,
@@ -361,9 +365,6 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a)
             p[j] *= by;
     } else {
         sigmoid_each(l, p);
-#pragma unroll
-        for (int j = 0; j < NE; ++j)
-            p[j] = (l[j] == l[j]) ? p[j] : (S)0;
     }
 #pragma unroll
     for (int j = 0; j < NE; ++j) {

@@ -90,6 +90,18 @@ def test_select_scores_below_the_smallest_number_are_zero(softmax):
     assert w.tolist() == ([[2.5, 0, 0, 0]] * 3 if softmax else [[0.0] * 4] * 3)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_select_experts_without_a_score_come_last_and_weigh_exactly_nothing(dt):
+    low = [-np.inf, -1000.0, -200.0, -199.5, np.nan, np.finfo(np.float32).min]
+    l = np.array([low + [-90.0, 1.0, -81.0, -80.0, -79.5, 0.0]] * 2, np.float32)
+    l[1] = l[1, ::-1]
+    idx, w = run_select(l, None, dt, 12, False, 1, 1, 1, False, 1.0)
+    # by score, then all scores of 0 by their number, the NaN behind them
+    assert idx[0].tolist() == [7, 11, 10, 9, 8, 6, 0, 1, 2, 3, 5, 4]
+    assert idx[1].tolist() == [4, 0, 1, 2, 3, 5, 6, 8, 9, 10, 11, 7]
+    assert (w[:, :6] > 0).all() and (w[:, 6:] == 0).all()
+
+
 # ---------------------------------------------------------------------------
 # bf16 outputs at both ends of the range: rounded to nearest even, no tolerance where the fp32 value's
 # bits are defined

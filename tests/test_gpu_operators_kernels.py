@@ -198,3 +198,36 @@ def test_grouped_router_adds_both_halves_of_the_logits(T, H, E, parts):
         got = lay.debug_read(2, (T, E), torch.float64).cpu().numpy()
         np.testing.assert_allclose(got, logits, rtol=1e-11, atol=1e-11)
     lay.close()
+
+
+@pytest.mark.parametrize("T", [6, 40])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_grouped_router_of_tokens_that_are_not_finite(T, softmax):
+    from quantized_expert_ffn_topk_amd import synth
+    from tests import operators_ref as ref
+    from tests.gpu_common import Case
+    from tests.test_gpu_operators import U
+    H, E, k, G = 1024, 64, 6, 8
+    base = Case(14, T, H, 256, E, k, 0, r=2.5, n_distinct=1)
+    bits = base.x.copy()
+    bits[1, 7] = 0x7fc0                                  # NaN: every logit is NaN
+    bits[2, 9] = 0x7f80                                  # inf: every logit is inf or -inf
+    bits[3] = 0                                          # every logit is 0: all equal
+    bits[4] = synth.f32_to_bf16_bits(synth.bf16_bits_to_f32(bits[4]) * np.float32(3e4))   # scores at both ends
+    c = Case(14, T, H, 256, E, k, 0, r=2.5, n_distinct=1, x=bits)
+    lay = c.layer(max_tokens=T)
+    x = lay.x_tensor(c.x)
+    idx, w = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    for best, renorm in ((2, True), (1, False)):
+        d = abi.moe_route_desc(E, k, int(softmax), G, 4, best, int(renorm), 1.5)
+        abi.moe_router_topk_grouped(lay.ctx, d, x, T, lay.weights, idx, w)
+        torch.cuda.synchronize()
+        got = lay.debug_read(2, (T, E), torch.float64).cpu().numpy()
+        assert np.isnan(got[1]).all() and (got[3] == 0).all()
+        # choice and weights from the logits that the router made
+        want, ww, _ = ref.select(got, c.b, k, softmax, G, 4, best, renorm, 1.5)
+        assert np.array_equal(idx.cpu().numpy(), want)
+        np.testing.assert_allclose(w.cpu().numpy(), ww, rtol=2 * U, atol=2.0 ** -149)
+        assert (w[1] == 0).all() and all(len(set(r)) == k for r in idx.tolist())
+        assert not torch.isnan(w).any()
+    lay.close()

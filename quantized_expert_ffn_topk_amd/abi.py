@@ -25,13 +25,14 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "moe.h")
 
 OK, E_INVAL, E_UNSUPPORTED, E_NOMEM, E_HIP, E_CAPACITY = range(6)
 WFMT_INT4, WFMT_MXFP4 = 0, 1
-DT_F32, DT_BF16 = 0, 1
+DT_F32, DT_BF16, DT_FP8 = 0, 1, 2
 PATH_AUTO, PATH_GEMV, PATH_MFMA, PATH_MX_BF16 = 0, 1, 2, 3
 CACHE_GLOBAL_LRU, CACHE_PER_LAYER_LRU = 0, 1
 CACHE_BACKEND_HIP, CACHE_BACKEND_HOST = 0, 1
 STAGE_DEMAND, STAGE_PREFETCH, STAGE_PREFETCH_IDLE = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+ACT_NONE, ACT_SWIGLU = 0, 1
 
 _NAMES = {OK: "OK", E_INVAL: "E_INVAL", E_UNSUPPORTED: "E_UNSUPPORTED", E_NOMEM: "E_NOMEM",
           E_HIP: "E_HIP", E_CAPACITY: "E_CAPACITY"}
@@ -121,6 +122,12 @@ def _declare(L):
         "moe_route_select": (st, [P(moe_route_desc), vp, i32, i64, vp, i32, vp, vp, vp]),
         "moe_router_topk_grouped": (st, [vp, P(moe_route_desc), vp, i32, P(moe_layer_weights), vp,
                                          vp, vp]),
+        "moe_quant_fp8": (st, [vp, i32, i64, i32, i32, i32, vp, vp, i64, vp, i64, vp]),
+        "moe_linear_fp8": (st, [vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i32, i32, vp, i32, i64, vp]),
+        "moe_grouped_linear": (st, [vp, i32, i64, vp, i64, i32, vp, vp, i32, i32, vp, i64, i64, vp, i64,
+                                    i64, i32, i32, vp, i32, i64, vp]),
+        "moe_group_rows": (st, [vp, i32, i32, i32, vp, vp, vp, vp]),
+        "moe_combine_rows": (st, [vp, i32, i64, i32, vp, vp, vp, i64, i32, i32, i32, vp, i32, i64, vp]),
         "moe_cache_create": (st, [P(moe_cache_desc), P(vp)]),
         "moe_cache_destroy": (None, [vp]),
         "moe_cache_stage": (st, [vp, i32, vp, i32, i32, vp, vp]),
@@ -307,7 +314,8 @@ def calls():
             m.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in m.NAMES), check, addr)
         else:
             m = types.SimpleNamespace(**{n: _through_ctypes(n) for n in (
-                "moe_rmsnorm_quant", "moe_swiglu_quant", "moe_linear_int8", "moe_route_select")})
+                "moe_rmsnorm_quant", "moe_swiglu_quant", "moe_linear_int8", "moe_route_select", "moe_quant_fp8",
+                "moe_linear_fp8", "moe_grouped_linear", "moe_group_rows", "moe_combine_rows")})
         _calls = m
     return _calls
 
@@ -328,6 +336,29 @@ def moe_linear_int8(q, ldq, s, T, w, ldw, ws, bias, N, K, out, out_dtype, ldo, s
 
 def moe_route_select(desc, logits, logit_dtype, ld, bias, T, idx, gate_w, stream=None):
     (_calls or calls()).moe_route_select(desc, logits, logit_dtype, ld, bias, T, idx, gate_w, stream)
+
+
+def moe_quant_fp8(x, x_dtype, ldx, act, T, K, count, q, ldq, s, lds, stream=None):
+    (_calls or calls()).moe_quant_fp8(x, x_dtype, ldx, act, T, K, count, q, ldq, s, lds, stream)
+
+
+def moe_linear_fp8(q, ldq, s, lds, T, w, ldw, ws, ldws, bias, N, K, out, out_dtype, ldo, stream=None):
+    (_calls or calls()).moe_linear_fp8(q, ldq, s, lds, T, w, ldw, ws, ldws, bias, N, K, out, out_dtype, ldo, stream)
+
+
+def moe_grouped_linear(x, x_dtype, ldx, s, lds, R, rows, offsets, E, M, w, ldw, w_stride, ws, ldws,
+                       ws_stride, N, K, out, out_dtype, ldo, stream=None):
+    (_calls or calls()).moe_grouped_linear(x, x_dtype, ldx, s, lds, R, rows, offsets, E, M, w, ldw, w_stride, ws,
+                                           ldws, ws_stride, N, K, out, out_dtype, ldo, stream)
+
+
+def moe_group_rows(idx, T, k, E, offsets, rows, pos, stream=None):
+    (_calls or calls()).moe_group_rows(idx, T, k, E, offsets, rows, pos, stream)
+
+
+def moe_combine_rows(y, y_dtype, ldy, R, pos, gate_w, base, ldb, T, k, H, out, out_dtype, ldo, stream=None):
+    (_calls or calls()).moe_combine_rows(y, y_dtype, ldy, R, pos, gate_w, base, ldb, T, k, H, out, out_dtype, ldo,
+                                         stream)
 
 
 def moe_router_topk_grouped(ctx, desc, x, T, weights, idx, gate_w, stream=None):

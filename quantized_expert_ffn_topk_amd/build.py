@@ -26,7 +26,8 @@ CXX = os.environ.get("CXX", "g++")
 
 HIP_SOURCES = ["kernels_router.hip", "kernels_gemv.hip", "kernels_bs1.hip", "kernels_gemm.hip",
                "kernels_mx.hip", "noalloc.hip", "kernels_probe.hip", "kernels_rows.hip",
-               "kernels_linear.hip", "kernels_route.hip"]
+               "kernels_linear.hip", "kernels_route.hip", "kernels_fp8.hip", "kernels_products.hip",
+               "kernels_dispatch.hip"]
 CPP_SOURCES = ["api.cpp", "pack.cpp", "cache.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fno-fast-math", "-Wall",

@@ -45,26 +45,6 @@ struct RowOut {
     int T, n;
 };
 
-// silu(g)*u in fp32, from E = exp(-|g|) <= 1 so that nothing overflows:
-// g*u/(1+E) for g >= 0, g*u*E/(1+E) for g < 0.  E is the square of 2^t with
-// t = -|g|*log2(e)/2 as a rounded product and its remainder r, so that the
-// exponent's rounding does not grow with |g| and E reaches the subnormals,
-// which the hardware's 2^t itself does not; the reciprocal is the hardware's
-// (one unit in the last place), of a number in [1,2].  Past |g| = 200 E is 0
-// either way.
-__device__ __forceinline__ float silu_mul(float g, float u)
-{
-    const float C = 0.72134751f, C_LO = 9.62981515e-9f;       // log2(e)/2 = C + C_LO
-    const float a = fminf(fabsf(g), 200.0f);
-    const float t = -a * C;
-    const float r = fmaf(-a, C_LO, fmaf(-a, C, -t));
-    const float h = __builtin_amdgcn_exp2f(t);
-    float e = h * h;
-    e = fmaf(e, r * 1.386294361f, e);                         // (1 + r ln 2)^2
-    const float d = __builtin_amdgcn_rcpf(1.0f + e);
-    return g * ((g < 0.0f) ? e * d : d) * u;
-}
-
 // ---------------------------------------------------------------------------
 // One row by NT threads, NV vectors of 8 values per thread (8*NT*NV >= n >= 8),
 // the row in registers between its one read and its writes.  A thread's vector

@@ -1,5 +1,6 @@
 // ops_common.h -- pieces shared by the operators around the MoE layer
-// (kernels_rows.hip, kernels_linear.hip, kernels_route.hip): argument checks,
+// (kernels_rows.hip, kernels_linear.hip, kernels_route.hip, kernels_fp8.hip,
+// kernels_products.hip, kernels_dispatch.hip): argument checks,
 // loads and stores of rows of any alignment, type conversions.
 #pragma once
 
@@ -149,6 +150,26 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     }
     *reinterpret_cast<bytes16_a4 *>(p) = a;
     *reinterpret_cast<bytes16_a4 *>(p + 4) = b;
+}
+
+// silu(g)*u in fp32, from E = exp(-|g|) <= 1 so that nothing overflows:
+// g*u/(1+E) for g >= 0, g*u*E/(1+E) for g < 0.  E is the square of 2^t with
+// t = -|g|*log2(e)/2 as a rounded product and its remainder r, so that the
+// exponent's rounding does not grow with |g| and E reaches the subnormals,
+// which the hardware's 2^t itself does not; the reciprocal is the hardware's
+// (one unit in the last place), of a number in [1,2].  Past |g| = 200 E is 0
+// either way.
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    const float C = 0.72134751f, C_LO = 9.62981515e-9f;       // log2(e)/2 = C + C_LO
+    const float a = fminf(fabsf(g), 200.0f);
+    const float t = -a * C;
+    const float r = fmaf(-a, C_LO, fmaf(-a, C, -t));
+    const float h = __builtin_amdgcn_exp2f(t);
+    float e = h * h;
+    e = fmaf(e, r * 1.386294361f, e);                         // (1 + r ln 2)^2
+    const float d = __builtin_amdgcn_rcpf(1.0f + e);
+    return g * ((g < 0.0f) ? e * d : d) * u;
 }
 
 // LDS written by lanes of a wave and read by others of the same wave

@@ -20,6 +20,11 @@ decltype(&moe_rmsnorm_quant) rmsnorm_quant;
 decltype(&moe_swiglu_quant) swiglu_quant;
 decltype(&moe_linear_int8) linear_int8;
 decltype(&moe_route_select) route_select;
+decltype(&moe_quant_fp8) quant_fp8;
+decltype(&moe_linear_fp8) linear_fp8;
+decltype(&moe_grouped_linear) grouped_linear;
+decltype(&moe_group_rows) group_rows;
+decltype(&moe_combine_rows) combine_rows;
 PyObject *check, *addr;                        // of abi
 PyObject *name_data_ptr, *name_cuda_stream;
 
@@ -224,17 +229,135 @@ PyObject *py_route_select(PyObject *, PyObject *const *v, Py_ssize_t n)
     return called(a, [&] { return route_select(&d, logits, dt, ld, bias, T, idx, w, st); });
 }
 
-// bind(addresses of the four in NAMES' order, abi.check, abi.addr)
+PyObject *py_quant_fp8(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    Args a(v, n, 12);
+    const void *x = a.ptr();
+    const int32_t xd = a.i32();
+    const int64_t ldx = a.i64();
+    const int32_t act = a.i32(), T = a.i32(), K = a.i32();
+    const int32_t *count = (const int32_t *)a.ptr();
+    void *q = a.ptr();
+    const int64_t ldq = a.i64();
+    float *s = (float *)a.ptr();
+    const int64_t lds = a.i64();
+    void *st = a.stream();
+    return called(a, [&] { return quant_fp8(x, xd, ldx, act, T, K, count, q, ldq, s, lds, st); });
+}
+
+PyObject *py_linear_fp8(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    Args a(v, n, 16);
+    const void *q = a.ptr();
+    const int64_t ldq = a.i64();
+    const float *s = (const float *)a.ptr();
+    const int64_t lds = a.i64();
+    const int32_t T = a.i32();
+    const void *w = a.ptr();
+    const int64_t ldw = a.i64();
+    const float *ws = (const float *)a.ptr();
+    const int64_t ldws = a.i64();
+    const float *bias = (const float *)a.ptr();
+    const int32_t N = a.i32(), K = a.i32();
+    void *out = a.ptr();
+    const int32_t od = a.i32();
+    const int64_t ldo = a.i64();
+    void *st = a.stream();
+    return called(a, [&] {
+        return linear_fp8(q, ldq, s, lds, T, w, ldw, ws, ldws, bias, N, K, out, od, ldo, st);
+    });
+}
+
+PyObject *py_grouped_linear(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    Args a(v, n, 22);
+    const void *x = a.ptr();
+    const int32_t xd = a.i32();
+    const int64_t ldx = a.i64();
+    const float *s = (const float *)a.ptr();
+    const int64_t lds = a.i64();
+    const int32_t R = a.i32();
+    const int32_t *rows = (const int32_t *)a.ptr(), *offsets = (const int32_t *)a.ptr();
+    const int32_t E = a.i32(), M = a.i32();
+    const void *w = a.ptr();
+    const int64_t ldw = a.i64(), w_stride = a.i64();
+    const float *ws = (const float *)a.ptr();
+    const int64_t ldws = a.i64(), ws_stride = a.i64();
+    const int32_t N = a.i32(), K = a.i32();
+    void *out = a.ptr();
+    const int32_t od = a.i32();
+    const int64_t ldo = a.i64();
+    void *st = a.stream();
+    return called(a, [&] {
+        return grouped_linear(x, xd, ldx, s, lds, R, rows, offsets, E, M, w, ldw, w_stride, ws, ldws, ws_stride, N,
+                              K, out, od, ldo, st);
+    });
+}
+
+PyObject *py_group_rows(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    Args a(v, n, 8);
+    const int32_t *idx = (const int32_t *)a.ptr();
+    const int32_t T = a.i32(), k = a.i32(), E = a.i32();
+    int32_t *offsets = (int32_t *)a.ptr(), *rows = (int32_t *)a.ptr(), *pos = (int32_t *)a.ptr();
+    void *st = a.stream();
+    return called(a, [&] { return group_rows(idx, T, k, E, offsets, rows, pos, st); });
+}
+
+PyObject *py_combine_rows(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    Args a(v, n, 15);
+    const void *y = a.ptr();
+    const int32_t yd = a.i32();
+    const int64_t ldy = a.i64();
+    const int32_t R = a.i32();
+    const int32_t *pos = (const int32_t *)a.ptr();
+    const float *w = (const float *)a.ptr();
+    const void *base = a.ptr();
+    const int64_t ldb = a.i64();
+    const int32_t T = a.i32(), k = a.i32(), H = a.i32();
+    void *out = a.ptr();
+    const int32_t od = a.i32();
+    const int64_t ldo = a.i64();
+    void *st = a.stream();
+    return called(a, [&] { return combine_rows(y, yd, ldy, R, pos, w, base, ldb, T, k, H, out, od, ldo, st); });
+}
+
+// the functions in NAMES' order
+const char *const NAMES[] = {"moe_rmsnorm_quant", "moe_swiglu_quant", "moe_linear_int8",
+                             "moe_route_select",  "moe_quant_fp8",    "moe_linear_fp8",
+                             "moe_grouped_linear", "moe_group_rows",  "moe_combine_rows"};
+constexpr Py_ssize_t N_NAMES = sizeof(NAMES) / sizeof(NAMES[0]);
+
+template <typename F>
+void set_function(F &f, unsigned long long at)
+{
+    f = (F)(uintptr_t)at;
+}
+
+// bind(addresses of the functions, abi.check, abi.addr)
 PyObject *py_bind(PyObject *, PyObject *args)
 {
-    unsigned long long f[4];
-    PyObject *c, *d;
-    if (!PyArg_ParseTuple(args, "KKKKOO", &f[0], &f[1], &f[2], &f[3], &c, &d))
+    if (PyTuple_GET_SIZE(args) != N_NAMES + 2) {
+        PyErr_Format(PyExc_TypeError, "%zd arguments, %zd wanted", PyTuple_GET_SIZE(args), N_NAMES + 2);
         return nullptr;
-    rmsnorm_quant = (decltype(rmsnorm_quant))(uintptr_t)f[0];
-    swiglu_quant = (decltype(swiglu_quant))(uintptr_t)f[1];
-    linear_int8 = (decltype(linear_int8))(uintptr_t)f[2];
-    route_select = (decltype(route_select))(uintptr_t)f[3];
+    }
+    unsigned long long f[N_NAMES];
+    for (Py_ssize_t i = 0; i < N_NAMES; ++i) {
+        f[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(args, i));
+        if (PyErr_Occurred())
+            return nullptr;
+    }
+    set_function(rmsnorm_quant, f[0]);
+    set_function(swiglu_quant, f[1]);
+    set_function(linear_int8, f[2]);
+    set_function(route_select, f[3]);
+    set_function(quant_fp8, f[4]);
+    set_function(linear_fp8, f[5]);
+    set_function(grouped_linear, f[6]);
+    set_function(group_rows, f[7]);
+    set_function(combine_rows, f[8]);
+    PyObject *c = PyTuple_GET_ITEM(args, N_NAMES), *d = PyTuple_GET_ITEM(args, N_NAMES + 1);
     Py_INCREF(c);
     Py_XSETREF(check, c);
     Py_INCREF(d);
@@ -248,6 +371,11 @@ PyMethodDef methods[] = {
     {"moe_swiglu_quant", (PyCFunction)(void (*)(void))py_swiglu_quant, METH_FASTCALL, nullptr},
     {"moe_linear_int8", (PyCFunction)(void (*)(void))py_linear_int8, METH_FASTCALL, nullptr},
     {"moe_route_select", (PyCFunction)(void (*)(void))py_route_select, METH_FASTCALL, nullptr},
+    {"moe_quant_fp8", (PyCFunction)(void (*)(void))py_quant_fp8, METH_FASTCALL, nullptr},
+    {"moe_linear_fp8", (PyCFunction)(void (*)(void))py_linear_fp8, METH_FASTCALL, nullptr},
+    {"moe_grouped_linear", (PyCFunction)(void (*)(void))py_grouped_linear, METH_FASTCALL, nullptr},
+    {"moe_group_rows", (PyCFunction)(void (*)(void))py_group_rows, METH_FASTCALL, nullptr},
+    {"moe_combine_rows", (PyCFunction)(void (*)(void))py_combine_rows, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "The operators around the layer, called directly.",
@@ -264,8 +392,14 @@ PyMODINIT_FUNC PyInit__calls(void)
     PyObject *m = PyModule_Create(&module);
     if (!m)
         return nullptr;
-    PyObject *names = Py_BuildValue("(ssss)", "moe_rmsnorm_quant", "moe_swiglu_quant", "moe_linear_int8",
-                                    "moe_route_select");
+    PyObject *names = PyTuple_New(N_NAMES);
+    for (Py_ssize_t i = 0; names && i < N_NAMES; ++i) {
+        PyObject *name = PyUnicode_FromString(NAMES[i]);
+        if (!name)
+            Py_CLEAR(names);
+        else
+            PyTuple_SET_ITEM(names, i, name);
+    }
     if (!names || PyModule_AddObject(m, "NAMES", names) != 0) {
         Py_XDECREF(names);
         Py_DECREF(m);

@@ -198,17 +198,46 @@ __device__ __forceinline__ v4i load_piece_end(const uint8_t *row, int k, int K)
     }
     return v;
 }
-// 16 (4) bytes of each active lane from memory to LDS at 16 (4) times the lane
-__device__ __forceinline__ void copy16(const void *from, void *to)
+// an address that is the same in every lane, in scalar registers
+__device__ __forceinline__ const uint8_t *uniform(const void *p)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+    return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ void copy4(const void *from, void *to)
+// `bytes` of memory at p as the load unit's buffer: what lies outside reads as 0, and
+// is not read
+__device__ __forceinline__ v4i buffer_of(const uint8_t *p, uint32_t bytes)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)to, 4, 0, 0);
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)u),
+               __builtin_amdgcn_readfirstlane((int)((uint32_t)(u >> 32) & 0xffff)),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
+// 16 bytes of each lane, at lane_at + at of a buffer, to LDS address `to` + 16 * lane.
+// In assembly: told of copies into LDS, the compiler waits for those on their way
+// before it reads LDS elsewhere, unless it can tell the places apart; here the
+// callers wait.  (m0 is the compiler's, and kept.)
+__device__ __forceinline__ void copy16(v4i from, uint32_t lane_at, int at, int to)
+{
+    int m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "buffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(lane_at), "s"(from), "s"(__builtin_amdgcn_readfirstlane(at))
+                 : "memory");
+}
+// the same of 4 bytes, from an address of each lane
+__device__ __forceinline__ void copy4(const void *from, int to)
+{
+    int m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
+                 : "memory");
+}
+constexpr int64_t NEAR = 1ll << 31;                  // bytes from a buffer's beginning that lane offsets reach
 
 // ---------------------------------------------------------------------------
 // A row's part of a stage in a lane: two pieces (32 bytes) of row l%16, the same
@@ -290,7 +319,7 @@ __device__ __forceinline__ void add_stage(v4f &acc, const Frag<MODE> &w, const F
 // stage comes.
 // ---------------------------------------------------------------------------
 template <int MODE, typename OT, bool GROUPED, bool NT, int RT, int TC, int W>
-__global__ __launch_bounds__(64 * W) void product_stream_kernel(ProdArgs a, int tiles_n)
+__global__ __launch_bounds__(64 * W, 2) void product_stream_kernel(ProdArgs a, int tiles_n)
 {
     constexpr int TB = (TC + 1) / 2;                 // 16-token tiles
     constexpr int CW = 2 * RT, CP = CW + TC;         // 8-row pieces per stage: weights, all
@@ -450,99 +479,117 @@ __global__ __launch_bounds__(64 * W) void product_stream_kernel(ProdArgs a, int 
 
 // ---------------------------------------------------------------------------
 // Tiles: a block computes BT = 16*WT*FT rows x BN = 16*WN*FN channels with WT*WN
-// waves of FT*FN 16x16 results, K in stages of 128 bytes through NB LDS buffers,
-// the next stages' rows on their way while one is multiplied.
+// waves of FT*FN 16x16 results (the rows' tiles go to the WT in turn), K in stages
+// of 128 bytes through NB LDS buffers, the next stages' rows on their way while one
+// is multiplied.
 // An LDS row is 128 bytes, eight pieces; piece c of row r sits at slot
 // c ^ (r/2 & 7): two rows fill the 64 banks once, so that 16 neighbouring rows'
 // reads of one piece fall on different banks.
 // DMA: rows go global -> LDS by the load unit (a wave's copy is 8 rows, lane l
 // writing slot l%8 of row l/8, so the lane picks the global piece that belongs
-// there); needs rows of 16-byte alignment.  Otherwise they pass through
-// registers.  The last, partial stage always does (load_piece_end's zeros).
+// there); needs rows of 16-byte alignment, not too far apart.  Otherwise they pass
+// through registers.  The last, partial stage always does (load_piece_end's zeros).
 // Scales: the weights' of all stages lie in LDS from the beginning, the rows'
 // come four stages at a time (16 bytes of a row of scales; one by one they would
-// be a line each), into one of two buffers while the other is read.
+// be a line each) into one of two places while the other is read.
 // ---------------------------------------------------------------------------
 constexpr int MAX_BLOCKS = 1024;                     // blocks of 128 codes in a row
 
-template <int MODE, typename OT, bool GROUPED, bool DMA, int NB, int WT, int WN, int FT, int FN>
-__global__ __launch_bounds__(64 * WT * WN) void product_tiles_kernel(ProdArgs a, int tiles_t, int tiles_n)
-{
-    constexpr int NW = WT * WN, BT = 16 * WT * FT, BN = 16 * WN * FN;
-    constexpr int CP = (BT + BN) / 8 / NW;           // 8-row copies per wave and stage
-    constexpr int TP = BT / 8 / NW;                  // of these, rows of x
-    constexpr int BUF = (BT + BN) * 128;             // bytes of a stage
-    constexpr bool SCALED = MODE != BF16;
-    constexpr int WB = BN > 128 ? BN / 128 : 1;      // blocks of 128 channels
-    constexpr int TPW = BT / NW;                     // rows whose scales a wave brings
-    static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 2 == 0, "whole copies per wave");
-    static_assert(16 * FN <= 128 && TPW <= 64, "a wave's channels share a scale");
-    static_assert(NB >= 2 && NB <= 4, "two to four buffers");
-    // the buffers are objects of their own: the compiler then knows that reads
-    // of one do not wait for copies into another
-    __shared__ __align__(128) uint8_t buf0[BUF];
-    __shared__ __align__(128) uint8_t buf1[BUF];
-    __shared__ __align__(128) uint8_t buf2[NB > 2 ? BUF : 16];
-    __shared__ __align__(128) uint8_t buf3[NB > 3 ? BUF : 16];
-    __shared__ __align__(16) float wscale[SCALED ? WB * MAX_BLOCKS : 4];
-    __shared__ __align__(16) float tscale0[SCALED ? 4 * BT : 4];
-    __shared__ __align__(16) float tscale1[SCALED ? 4 * BT : 4];
+// lambdas that hold a kernel's registers
+#define INLINE __attribute__((always_inline))
 
+// f(0), ..., f(N-1) with constants
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void steps_of(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        steps_of<N, I + 1>(f);
+    }
+}
+
+template <int MODE, int NB, int WT, int WN, int FT, int FN>
+struct TileShape {
+    static constexpr bool SCALED = MODE != BF16;
+    static constexpr int NW = WT * WN, BT = 16 * WT * FT, BN = 16 * WN * FN;
+    static constexpr int CP = (BT + BN) / 8 / NW;    // 8-row copies per wave and stage
+    static constexpr int TP = BT / 8 / NW;           // of these, rows of x
+    static constexpr int BUF = (BT + BN) * 128;      // bytes of a stage
+    static constexpr int WB = BN > 128 ? BN / 128 : 1;   // blocks of 128 channels
+    static constexpr int SROWS = BT < 64 ? 64 : BT;  // rows of scales in LDS
+    static constexpr int WSCALE = NB * BUF, TSCALE = WSCALE + (SCALED ? 4 * (WB * MAX_BLOCKS + 4) : 0);
+    static constexpr int LDS = TSCALE + (SCALED ? 2 * 16 * SROWS : 0);
+    static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 2 == 0, "whole copies per wave");
+    static_assert(16 * FN <= 128 && SROWS <= 64 * NW, "a wave's channels share a scale");
+    static_assert(NB >= 2 && LDS <= 160 * 1024, "the stages fit");
+};
+
+template <int MODE, typename OT, bool GROUPED, bool DMA, int NB, int WT, int WN, int FT, int FN>
+__device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, uint8_t *lds)
+{
+    typedef TileShape<MODE, NB, WT, WN, FT, FN> S;
+    constexpr bool SCALED = S::SCALED;
+    constexpr int NW = S::NW, BT = S::BT, CP = S::CP, TP = S::TP, BUF = S::BUF, SROWS = S::SROWS;
+    const float *wscale = reinterpret_cast<const float *>(lds + S::WSCALE);
+    const float *tscale = reinterpret_cast<const float *>(lds + S::TSCALE);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Tile t;
-    if constexpr (GROUPED) {
-        if (!find_tile<BT, BN>(a, tiles_n, lane, t))
-            return;
-    } else {
-        // tiles in groups of 8 row tiles, row tile fastest, each XCD (blocks with
-        // the same index mod 8) a contiguous run of them
-        const int per = gridDim.x >> 3, logical = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-        if (logical >= tiles_t * tiles_n)
-            return;
-        const int band = logical / (8 * tiles_n), in = logical - band * 8 * tiles_n;
-        const int gt = min(8, tiles_t - 8 * band);
-        t = Tile{(8 * band + in % gt) * BT, 0, (in / gt) * BN, a.w, a.ws};
-        t.rows = min(BT, a.M - t.row0);
-    }
+    const int lds0 = (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+    const int stages = a.K >> 7, blocks = (a.K + 127) >> 7;
+    const bool gathered = GROUPED && a.rows;
 
+    // copies
     const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));   // NW is even
-    const uint8_t *src[CP];                          // this lane's piece of each copy
+    auto row_of = [&](int i) INLINE {                // the row of copy i, before this lane's piece
+        const int r = 8 * (wave + NW * (i < TP ? i : i - TP)) + (lane >> 3);
+        return i < TP ? a.x + source_row<GROUPED>(a, t.row0 + min(r, t.rows - 1)) * a.ldx
+                      : t.w + (int64_t)min(t.n0 + r, a.N - 1) * a.ldw;
+    };
+    auto lds_at = [&](int i) INLINE { return (i < TP ? 0 : BT * 128) + 1024 * (wave + NW * (i < TP ? i : i - TP)); };
+    const uint8_t *x0 = uniform(gathered ? a.x : a.x + (int64_t)t.row0 * a.ldx);
+    const uint8_t *w0 = uniform(t.w + (int64_t)t.n0 * a.ldw);
+    uint32_t lane_at[DMA ? CP : 1];                  // this lane's piece of each copy
+    const uint8_t *src[DMA ? 1 : CP];
 #pragma unroll
     for (int i = 0; i < CP; ++i) {
-        const int r = 8 * (wave + NW * (i < TP ? i : i - TP)) + (lane >> 3);
-        src[i] = (i < TP) ? a.x + source_row<GROUPED>(a, t.row0 + min(r, t.rows - 1)) * a.ldx
-                          : t.w + (int64_t)min(t.n0 + r, a.N - 1) * a.ldw;
-        src[i] += 16 * piece;
+        if constexpr (DMA)
+            lane_at[i] = (uint32_t)(row_of(i) + 16 * piece - (i < TP ? x0 : w0));
+        else
+            src[i] = row_of(i) + 16 * piece;
     }
-    auto lds_at = [&](int i) { return (i < TP ? 0 : BT * 128) + 1024 * (wave + NW * (i < TP ? i : i - TP)); };
-    const int stages = a.K >> 7, blocks = (a.K + 127) >> 7;
-
-    // scales
-    const float *s_row = nullptr;
-    bool wide = false;                               // four scales of a row in one load
-    if constexpr (SCALED) {
-        s_row = a.s + source_row<GROUPED>(a, t.row0 + min(TPW * wave + min(lane, TPW - 1), t.rows - 1)) * a.lds;
-        wide = (reinterpret_cast<uintptr_t>(a.s) & 15) == 0 && (a.lds & 3) == 0;
-        for (int i = wave; i < WB * ((blocks + 63) >> 6); i += NW) {
-            const int b = i % WB, k = i / WB * 64;
-            const float *row = t.ws + (int64_t)(min(t.n0 + 128 * b, a.N - 1) >> 7) * a.ldws;
-            copy4(row + min(k + lane, blocks - 1), wscale + b * MAX_BLOCKS + k);
-        }
-    }
-    // the scales of stages 4*quad .. 4*quad+3: [row][4] where `wide` and all exist, else [4][row]
-    auto quad_wide = [&](int quad) { return wide && 4 * quad + 4 <= blocks; };
-    auto bring = [&](int quad) {
-        if (4 * quad >= blocks || lane >= TPW)
-            return;
-        float *to = (quad & 1) ? tscale1 : tscale0;
-        if (quad_wide(quad)) {
-            copy16(s_row + 4 * quad, to + 4 * TPW * wave);
-        } else {
+    v4i reg[DMA ? 1 : CP];
+    auto fetch = [&](int i, int buf, int st) INLINE {    // sets out copy i of stage st
+        if constexpr (DMA)
+            copy16(buffer_of(i < TP ? x0 : w0, st < stages ? 0xffffffffu : 0u), lane_at[i], 128 * st, lds0 + buf + lds_at(i));
+        else
+            reg[i] = load_piece(src[i] + 128 * min(st, stages - 1));
+    };
+    auto land = [&](int buf) INLINE {
+        if constexpr (!DMA) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                copy4(s_row + min(4 * quad + c, blocks - 1), to + c * BT + TPW * wave);
+            for (int i = 0; i < CP; ++i)
+                *reinterpret_cast<v4i *>(lds + buf + lds_at(i) + 16 * lane) = reg[i];
         }
+    };
+
+    // scales: a quad is those of four stages, in LDS as [row][4]
+    v4i s_rows = {0, 0, 0, 0};
+    uint32_t s_lane = 0;
+    if constexpr (SCALED) {
+        const float *s0 = gathered ? a.s : a.s + (int64_t)t.row0 * a.lds;
+        const int r = min(64 * wave + lane, t.rows - 1);
+        s_lane = (uint32_t)((gathered ? source_row<GROUPED>(a, t.row0 + r) : r) * a.lds * 4);
+        // its end is the last row's: what a quad has past it reads as 0
+        s_rows = buffer_of(uniform(s0), (uint32_t)(((int64_t)((gathered ? a.R : t.rows) - 1) * a.lds + blocks) * 4));
+        for (int i = wave; i < S::WB * ((blocks + 63) >> 6); i += NW) {
+            const int b = i % S::WB, k = i / S::WB * 64;
+            const float *row = t.ws + (int64_t)(min(t.n0 + 128 * b, a.N - 1) >> 7) * a.ldws;
+            copy4(row + min(k + lane, blocks - 1), lds0 + S::WSCALE + 4 * (b * MAX_BLOCKS + k));
+        }
+    }
+    auto bring = [&](int q) INLINE {                 // sets out a quad's copy
+        if (SCALED && 64 * wave < BT && 4 * q < blocks)
+            copy16(s_rows, s_lane, 16 * q, lds0 + S::TSCALE + 16 * (SROWS * (q & 1) + 64 * wave));
     };
 
     v4f acc[FT][FN];
@@ -556,134 +603,166 @@ __global__ __launch_bounds__(64 * WT * WN) void product_tiles_kernel(ProdArgs a,
 #pragma unroll
     for (int u = 0; u < 2; ++u)
         at[u] = 128 * (lane & 15) + 16 * ((4 * u + (lane >> 4)) ^ ((lane >> 1) & 7));
-    const int x_at = 2048 * FT * wt, w_at = BT * 128 + 2048 * FN * wn;
-    auto read_x = [&](Frag<MODE> &f, const uint8_t *buf, int i) {
-        f.set(*reinterpret_cast<const v4i *>(buf + at[0] + x_at + 2048 * i),
-              *reinterpret_cast<const v4i *>(buf + at[1] + x_at + 2048 * i));
+    const int x_at = 2048 * wt, w_at = BT * 128 + 2048 * FN * wn;
+    auto read_x = [&](Frag<MODE> &f, int buf, int i) INLINE {
+        f.set(*reinterpret_cast<const v4i *>(lds + buf + at[0] + x_at + 2048 * WT * i),
+              *reinterpret_cast<const v4i *>(lds + buf + at[1] + x_at + 2048 * WT * i));
     };
-    auto read_w = [&](Frag<MODE> &f, const uint8_t *buf, int j) {
-        f.set(*reinterpret_cast<const v4i *>(buf + at[0] + w_at + 2048 * j),
-              *reinterpret_cast<const v4i *>(buf + at[1] + w_at + 2048 * j));
-    };
-    float sc[FT];
-    auto read_scales = [&](int st) {                 // of stage st, for this lane's rows
-        if constexpr (SCALED) {
-            const float *q = ((st >> 2) & 1) ? tscale1 : tscale0;
-            const bool w4 = quad_wide(st >> 2);
-            const int step = w4 ? 4 : 1, first = w4 ? (st & 3) : (st & 3) * BT;
-            const float ws = wscale[(16 * FN * wn >> 7) * MAX_BLOCKS + st];
-#pragma unroll
-            for (int i = 0; i < FT; ++i)
-                sc[i] = q[first + step * (16 * (FT * wt + i) + (lane & 15))] * ws;
-        }
+    auto read_w = [&](Frag<MODE> &f, int buf, int j) INLINE {
+        f.set(*reinterpret_cast<const v4i *>(lds + buf + at[0] + w_at + 2048 * j),
+              *reinterpret_cast<const v4i *>(lds + buf + at[1] + w_at + 2048 * j));
     };
 
-    v4i reg[DMA ? 1 : CP];
-    auto fetch = [&](uint8_t *buf) {                 // sets out the next whole stage
+    // A stage is FT steps, a step the products of one tile of rows with the FN of
+    // channels.  x and its scales are read LA steps ahead, w in the stage's last step,
+    // each in the place of the fragment that was just used; products are scaled and
+    // added LAG products later.  Before step TURN, whose x is the next stage's, nothing
+    // of this stage is left to be read but w: the waves meet, and stage st + NB sets
+    // out over it, a copy at a time between the products (all at once they fill the
+    // load unit's queue, and what is behind them waits).
+    constexpr int XR = FT % 4 == 0 ? 4 : FT % 3 == 0 ? 3 : 2, LA = XR - 1, TURN = FT - LA, LAG = 2, SLOTS = LA * FN;
+    static_assert(FT % XR == 0 && FT % 2 == 0 && FN % LAG == 0, "places change the same way in each stage");
+    Frag<MODE> wf[FN], xf[XR];
+    v4f p[LAG];                                      // products not yet added
+    float sv[XR], sc[2] = {0.0f, 0.0f};              // scales of rows; of this step and the one before
+    float ws = 1.0f, ws_next = 1.0f;
+    int s_at = 0;                                    // of the stage and this lane's rows, in tscale
 #pragma unroll
-        for (int i = 0; i < CP; ++i) {
-            if constexpr (DMA)
-                copy16(src[i], buf + lds_at(i));
-            else
-                reg[i] = load_piece(src[i]);
-            src[i] += 128;
-        }
+    for (int j = 0; j < LAG; ++j)
+        p[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto read_s = [&](int i) INLINE {
+        if constexpr (SCALED)
+            sv[i % XR] = tscale[s_at + 64 * WT * i];
     };
-    auto land = [&](uint8_t *buf) {
-        if constexpr (!DMA) {
-#pragma unroll
-            for (int i = 0; i < CP; ++i)
-                *reinterpret_cast<v4i *>(buf + lds_at(i) + 16 * lane) = reg[i];
+    auto scales_of = [&](int st) INLINE {
+        if constexpr (SCALED) {
+            ws_next = wscale[(16 * FN * wn >> 7) * MAX_BLOCKS + st];
+            s_at = ((st >> 2) & 1) * 4 * SROWS + (st & 3) + 4 * (16 * wt + (lane & 15));
         }
     };
     // this wave's copies have landed but for those of the LEFT stages set out
-    // last, and its reads are done; then every wave's
-    auto meet = [&](auto left_) {
+    // last, and its reads are done; then every wave's.  (Where rows pass through
+    // registers, loads stay on their way.)
+    auto meet = [&](auto left_) INLINE {
         constexpr int LEFT = decltype(left_)::value * CP;
         static_assert(LEFT < 64, "vmcnt counts to 63");
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);   // vmcnt(LEFT) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(DMA ? 0x0070 | (LEFT & 15) | (LEFT >> 4) << 14    // vmcnt(LEFT) lgkmcnt(0)
+                                       : 0xc07f);                                    // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    const std::integral_constant<int, 0> all;
-    Frag<MODE> wf[FN], xf[2];
-    // a stage whose rows are in buf
-    auto multiply_stage = [&](const uint8_t *buf, int st) {
-        read_scales(st);
+    // the product LAG before product m of a stage
+    auto add = [&](auto m_, float now, float before) INLINE {
+        if constexpr (SCALED) {
+            constexpr int m = decltype(m_)::value, of = (m - LAG + FT * FN) % (FT * FN), i = of / FN, j = of % FN;
+            const float s = (i == m / FN) ? now : before;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = fmaf(p[m % LAG][e], s, acc[i][j][e]);
+            // here, and not where the compiler would sink it to: before the next stage's
+            asm volatile("" : "+v"(acc[i][j]));
+        }
+    };
+    // stage st, whose rows are in cur; LAST: none is read ahead
+    auto run_stage = [&](auto last_, int cur, int next, int st) INLINE {
+        constexpr bool LAST = decltype(last_)::value;
+        ws = ws_next;
+        steps_of<FT>([&](auto i_) INLINE {
+            constexpr int i = decltype(i_)::value;
+            sc[i & 1] = sv[i % XR] * ws;
+            if constexpr (i == TURN && !LAST) {
+                land(next);
+                meet(std::integral_constant<int, NB - 2>());
+                if (SCALED && (st & 3) == 3)         // its quad's place is free
+                    bring((st >> 2) + 2);
+                scales_of(st + 1);
+            }
+            if constexpr (i < TURN) {
+                read_x(xf[(i + LA) % XR], cur, i + LA);
+                read_s(i + LA);
+            } else if constexpr (!LAST) {
+                read_x(xf[(i + LA) % XR], next, i + LA - FT);
+                read_s(i + LA - FT);
+            }
+            steps_of<FN>([&](auto j_) INLINE {
+                constexpr int j = decltype(j_)::value, m = FN * i + j, slot = m - FN * TURN;
+                if constexpr (SCALED) {
+                    add(std::integral_constant<int, m>(), sc[i & 1], sc[1 - (i & 1)]);
+                    p[m % LAG] = stage_product<MODE>(wf[j], xf[i % XR], v4f{0.0f, 0.0f, 0.0f, 0.0f});
+                } else {
+                    acc[i][j] = stage_product<MODE>(wf[j], xf[i % XR], acc[i][j]);
+                }
+                if constexpr (i >= TURN && !LAST) {
+#pragma unroll
+                    for (int c = slot * CP / SLOTS; c < (slot + 1) * CP / SLOTS; ++c)
+                        fetch(c, cur, st + NB);
+                    if constexpr (i == FT - 1)
+                        read_w(wf[j], next, j);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        });
+    };
+    auto begin = [&](int buf, int st) INLINE {
+        scales_of(st);
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            read_x(xf[i], buf, i);
+            read_s(i);
+        }
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             read_w(wf[j], buf, j);
-        read_x(xf[0], buf, 0);
-#pragma unroll
-        for (int i = 0; i < FT; ++i) {
-            if (i + 1 < FT)
-                read_x(xf[(i + 1) & 1], buf, i + 1);
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                add_stage<MODE>(acc[i][j], wf[j], xf[i & 1], sc[i]);
-        }
     };
-    if constexpr (SCALED) {
-        bring(0);
-        bring(1);
-    }
-    auto buf = [&](int i) { return i == 0 ? buf0 : i == 1 ? buf1 : i == 2 ? buf2 : buf3; };
-    if constexpr (DMA) {
+    const std::false_type more;
+    const std::true_type last;
+    bring(0);
+    bring(1);
+    if (stages > 0) {
+        // registers hold one stage, so that there is one less on its way
 #pragma unroll
-        for (int i = 0; i < NB - 1; ++i)
-            if (i < stages)
-                fetch(buf(i));
-        for (int st = 0; st < stages; st += NB) {
+        for (int b = 0; b < (DMA ? NB : 2); ++b) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                if (st + i >= stages)
-                    break;
-                // stage st+i has landed, and everyone is done with the stage before
-                if (st + i + NB - 2 < stages)
-                    meet(std::integral_constant<int, NB - 2>());
-                else
-                    meet(all);
-                if (st + i + NB - 1 < stages)
-                    fetch(buf((i + NB - 1) % NB));
-                if (SCALED && ((st + i) & 3) == 0 && st + i > 0)
-                    bring(((st + i) >> 2) + 1);
-                multiply_stage(buf(i), st + i);
-            }
+            for (int i = 0; i < CP; ++i)
+                fetch(i, b * BUF, b);
+            if (b == 0)
+                land(0);
         }
-    } else {
-        if (stages > 0)
-            fetch(buf0);
+        meet(std::integral_constant<int, NB - 1>());
+        begin(0, 0);
+        int cur = 0;
         for (int st = 0; st < stages; ++st) {
-            uint8_t *cur = (st & 1) ? buf1 : buf0;
-            land(cur);
-            if (st + 1 < stages)
-                fetch(nullptr);
-            __syncthreads();
-            if (SCALED && (st & 3) == 0 && st > 0)
-                bring((st >> 2) + 1);
-            multiply_stage(cur, st);
+            const int next = (cur == (NB - 1) * BUF) ? 0 : cur + BUF;
+            run_stage(more, cur, next, st);
+            cur = next;
         }
     }
-    __syncthreads();
     if (a.K & 127) {
-        const int k = 128 * stages + 16 * piece;     // src has come this far
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        const int k = 128 * stages + 16 * piece;
 #pragma unroll
         for (int i = 0; i < CP; ++i)
-            *reinterpret_cast<v4i *>(buf0 + lds_at(i) + 16 * lane) = load_piece_end(src[i] - k, k, a.K);
-        meet(all);
-        multiply_stage(buf0, stages);
+            *reinterpret_cast<v4i *>(lds + lds_at(i) + 16 * lane) = load_piece_end(row_of(i), k, a.K);
         __syncthreads();
+        begin(0, stages);
+        run_stage(last, 0, 0, stages);
     }
+    steps_of<LAG>([&](auto j_) INLINE { add(j_, 0.0f, sc[(FT - 1) & 1]); });
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);                   // copies past the end are still to land
+    __syncthreads();
 
     // Epilogue: a wave passes 16 rows x 16*FN channels at a time through LDS of its
     // own and writes them as 16 bytes per lane, whole rows of the wave's channels.
     constexpr int PITCH = 16 * FN * (int)sizeof(OT) + 16;
     constexpr int LPR = FN * (int)sizeof(OT);        // lanes (16 bytes each) per row
     constexpr int VE = 16 / (int)sizeof(OT);         // values per lane
-    static_assert(16 * PITCH * NW <= BUF, "the waves' parts fit a buffer");
-    const int nw0 = t.n0 + 16 * FN * wn, tw0 = 16 * FT * wt;
-    uint8_t *mine = buf0 + wave * 16 * PITCH;
+    static_assert(16 * PITCH * NW <= NB * BUF, "the waves' parts fit the buffers");
+    const int nw0 = t.n0 + 16 * FN * wn;
+    uint8_t *mine = lds + wave * 16 * PITCH;
     float bias[FN][4];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -710,7 +789,7 @@ __global__ __launch_bounds__(64 * WT * WN) void product_tiles_kernel(ProdArgs a,
 #pragma unroll
         for (int h = 0; h < (16 * LPR + 63) / 64; ++h) {
             const int f = 64 * h + lane, row = f / LPR, col = (f % LPR) * VE;
-            const int r = tw0 + 16 * i + row, n = nw0 + col;
+            const int r = 16 * (WT * i + wt) + row, n = nw0 + col;
             if (row < 16 && r < t.rows) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * PITCH + col * (int)sizeof(OT));
                 OT *o = static_cast<OT *>(a.out) + (int64_t)(t.row0 + r) * a.ldo + n;
@@ -729,10 +808,54 @@ __global__ __launch_bounds__(64 * WT * WN) void product_tiles_kernel(ProdArgs a,
     }
 }
 
+template <int MODE, typename OT, bool GROUPED, bool DMA, int NB, int WT, int WN, int FT, int FN>
+__global__ __launch_bounds__(64 * WT * WN, 2) void product_tiles_kernel(ProdArgs a, int tiles_t, int tiles_n)
+{
+    typedef TileShape<MODE, NB, WT, WN, FT, FN> S;
+    __shared__ __align__(128) uint8_t lds[S::LDS];
+    Tile t;
+    if constexpr (GROUPED) {
+        if (!find_tile<S::BT, S::BN>(a, tiles_n, threadIdx.x & 63, t))
+            return;
+    } else {
+        // tiles in groups of 8 row tiles, row tile fastest, each XCD (blocks with
+        // the same index mod 8) a contiguous run of them
+        const int per = gridDim.x >> 3, logical = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+        if (logical >= tiles_t * tiles_n)
+            return;
+        const int band = logical / (8 * tiles_n), in = logical - band * 8 * tiles_n;
+        const int gt = min(8, tiles_t - 8 * band);
+        t = Tile{(8 * band + in % gt) * S::BT, 0, (in / gt) * S::BN, a.w, a.ws};
+        t.rows = min(S::BT, a.M - t.row0);
+    }
+    tile_product<MODE, OT, GROUPED, DMA, NB, WT, WN, FT, FN>(a, t, lds);
+}
+
+// The rows of a group, up to 256 at a time, as a tile of as many as there are: 64, 128,
+// 192 or 256 x 256 channels.
+template <int MODE, typename OT, bool DMA>
+__global__ __launch_bounds__(512, 2) void product_groups_kernel(ProdArgs a, int tiles_n)
+{
+    __shared__ __align__(128) uint8_t lds[TileShape<MODE, 3, 2, 4, 4, 4>::LDS];
+    static_assert(TileShape<MODE, 2, 2, 4, 8, 4>::LDS <= sizeof(lds) && TileShape<MODE, 2, 2, 4, 6, 4>::LDS <= sizeof(lds) &&
+                  TileShape<MODE, 3, 2, 4, 2, 4>::LDS <= sizeof(lds), "every shape fits");
+    Tile t;
+    if (!find_tile<256, 256>(a, tiles_n, threadIdx.x & 63, t))
+        return;
+    if (t.rows <= 64)
+        tile_product<MODE, OT, true, DMA, 3, 2, 4, 2, 4>(a, t, lds);
+    else if (t.rows <= 128)
+        tile_product<MODE, OT, true, DMA, 3, 2, 4, 4, 4>(a, t, lds);
+    else if (t.rows <= 192)
+        tile_product<MODE, OT, true, DMA, 2, 2, 4, 6, 4>(a, t, lds);
+    else
+        tile_product<MODE, OT, true, DMA, 2, 2, 4, 8, 4>(a, t, lds);
+}
+
 // ---------------------------------------------------------------------------
 // Launches.
 // ---------------------------------------------------------------------------
-
+constexpr int64_t CUS = 256;
 
 static int64_t ceil_div(int64_t a, int64_t b)
 {
@@ -766,37 +889,134 @@ static void launch_tiles(const ProdArgs &a, hipStream_t st)
            64 * WT * WN, 0, st, a, (int)tt, tn);
 }
 
-template <int MODE, typename OT, bool GROUPED, bool DMA>
-static void enqueue_tiles(const ProdArgs &a, int64_t rows, hipStream_t st)
+template <int MODE, typename OT, bool DMA>
+static void launch_groups(const ProdArgs &a, hipStream_t st)
 {
-    launch_tiles<MODE, OT, GROUPED, DMA, DMA ? 4 : 2, 2, 2, 2, 2>(a, st);
+    const int tn = (int)ceil_div(a.N, 256);
+    const int64_t tt = row_tiles(a, true, 256);
+    launch(product_groups_kernel<MODE, OT, DMA>, (unsigned)ceil_div(tt * tn, 8) * 8, 512, 0, st, a, tn);
 }
 
-// rows: of a group on average
-template <int MODE, int TILE_MODE, typename OT, bool GROUPED>
-static void enqueue_product(const ProdArgs &a, hipStream_t st)
+// rows that the load unit can copy into LDS: on 4 bytes, and within reach
+static bool copies_rows(const ProdArgs &a)
 {
-    const int64_t rows = GROUPED ? ceil_div(a.M, a.E) : a.M;
-    if (rows <= 8)
-        launch_stream<MODE, OT, GROUPED, false, 2, 1, 4>(a, st);
-    else if (rows <= 16)
-        launch_stream<MODE, OT, GROUPED, false, 2, 2, 4>(a, st);
-    else if (rows <= 32)
-        launch_stream<MODE, OT, GROUPED, false, 2, 4, 4>(a, st);
-    else if (ops_aligned(a.x, 16) && ops_aligned(a.w, 16) && a.ldx % 16 == 0 && a.ldw % 16 == 0 && a.w_stride % 16 == 0)
-        enqueue_tiles<TILE_MODE, OT, GROUPED, true>(a, rows, st);
-    else
-        enqueue_tiles<TILE_MODE, OT, GROUPED, false>(a, rows, st);
+    return ops_aligned(a.x, 4) && ops_aligned(a.w, 4) && a.ldx % 4 == 0 && a.ldw % 4 == 0 && a.w_stride % 4 == 0 &&
+           a.ldw <= NEAR / 256 && a.ldx <= NEAR / (a.rows ? a.R : 256);
 }
 
-// E4M3: fp32 outputs take exact products everywhere
-template <bool GROUPED>
-static void enqueue_f8(const ProdArgs &a, int32_t out_dtype, hipStream_t st)
+struct TileCost {
+    int bt, bn;
+    double stage, fixed, alone;                      // us
+};
+
+// The tile whose rounds over the CUs cost least.
+template <size_t N>
+static int cheapest(const TileCost (&c)[N], const ProdArgs &a)
 {
-    if (out_dtype == MOE_DT_F32)
-        enqueue_product<F8X, F8X, float, GROUPED>(a, st);
-    else
-        enqueue_product<F8X, F8, bf16_t, GROUPED>(a, st);
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < (int)N; ++i) {
+        const int64_t n = ceil_div(ceil_div(a.M, c[i].bt) * ceil_div(a.N, c[i].bn), CUS);
+        const double stages = a.K / 128.0;
+        const double cost = n * (c[i].stage * stages + c[i].fixed) + (n % 2 ? c[i].alone * stages : 0.0);
+        if (i == 0 || cost < least) {
+            best = i;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+template <int MODE, typename OT>
+static void enqueue_dense_tiles(const ProdArgs &a, hipStream_t st)
+{
+    if (!copies_rows(a)) {
+        if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= CUS)
+            launch_tiles<MODE, OT, false, false, 2, 4, 2, 2, 4>(a, st);
+        else
+            launch_tiles<MODE, OT, false, false, 2, 2, 2, 2, 2>(a, st);
+        return;
+    }
+    if constexpr (MODE == F8) {
+        static constexpr TileCost cost[] = {{64, 64, 0.253, 1.5, 0.08}, {64, 128, 0.36, 2.2, 0.0}, {128, 128, 0.56, 3.5, 0.0},
+                                            {128, 256, 0.95, 4.0, 0.0}, {256, 256, 1.55, 7.0, 0.0}};
+        switch (cheapest(cost, a)) {
+        case 0: launch_tiles<MODE, OT, false, true, 4, 2, 2, 2, 2>(a, st); break;
+        case 1: launch_tiles<MODE, OT, false, true, 3, 2, 4, 2, 2>(a, st); break;
+        case 2: launch_tiles<MODE, OT, false, true, 3, 4, 2, 2, 4>(a, st); break;
+        case 3: launch_tiles<MODE, OT, false, true, 3, 2, 4, 4, 4>(a, st); break;
+        default: launch_tiles<MODE, OT, false, true, 2, 2, 4, 8, 4>(a, st); break;
+        }
+    } else {
+        static constexpr TileCost cost[] = {{64, 64, 0.305, 1.5, 0.2}, {64, 128, 0.52, 2.5, 0.2}, {128, 128, 1.02, 3.5, 0.0},
+                                            {128, 256, 1.65, 4.0, 0.0}};
+        switch (cheapest(cost, a)) {
+        case 0: launch_tiles<MODE, OT, false, true, 4, 2, 2, 2, 2>(a, st); break;
+        case 1: launch_tiles<MODE, OT, false, true, 3, 2, 4, 2, 2>(a, st); break;
+        case 2: launch_tiles<MODE, OT, false, true, 3, 4, 2, 2, 4>(a, st); break;
+        default: launch_tiles<MODE, OT, false, true, 3, 2, 4, 4, 4>(a, st); break;
+        }
+    }
+}
+
+template <int MODE, int TILE_MODE, typename OT>
+static void enqueue_dense(const ProdArgs &a, hipStream_t st)
+{
+    const auto blocks = [&](int t, int n) { return ceil_div(a.M, t) * ceil_div(a.N, n); };
+    if (a.M <= 8) {
+        if (blocks(8, 16) <= CUS)
+            launch_stream<MODE, OT, false, false, 1, 1, 16>(a, st);
+        else
+            launch_stream<MODE, OT, false, false, 1, 1, 8>(a, st);
+    } else if (a.M <= 16) {
+        if (blocks(16, 16) <= CUS)
+            launch_stream<MODE, OT, false, false, 1, 2, 8>(a, st);
+        else
+            launch_stream<MODE, OT, false, false, 2, 2, 8>(a, st);
+    } else if (blocks(32, 16) <= CUS) {
+        launch_stream<MODE, OT, false, false, 1, 4, 8>(a, st);
+    } else if (blocks(32, 32) <= CUS) {
+        launch_stream<MODE, OT, false, false, 2, 4, 8>(a, st);
+    } else if (a.M <= 32) {
+        launch_stream<MODE, OT, false, false, 2, 4, 4>(a, st);
+    } else {
+        enqueue_dense_tiles<TILE_MODE, OT>(a, st);
+    }
+}
+
+template <int MODE, int TILE_MODE, typename OT>
+static void enqueue_grouped(const ProdArgs &a, hipStream_t st)
+{
+    const int64_t rows = ceil_div(a.M, a.E);         // of a group on average
+    // weights that the last-level cache does not keep from one call to the next, and
+    // that hardly anyone reads twice
+    const bool passing = (int64_t)(a.E < a.M ? a.E : a.M) * a.N * a.K >= (512ll << 20);
+    if (rows <= 4) {
+        if (passing)
+            launch_stream<MODE, OT, true, true, 2, 2, 4>(a, st);
+        else
+            launch_stream<MODE, OT, true, false, 2, 2, 4>(a, st);
+    } else if (rows <= 12) {
+        if (passing)
+            launch_stream<MODE, OT, true, true, 4, 4, 4>(a, st);
+        else
+            launch_stream<MODE, OT, true, false, 4, 4, 4>(a, st);
+    } else if (!copies_rows(a)) {
+        if (rows >= 128)
+            launch_tiles<TILE_MODE, OT, true, false, 2, 4, 2, 2, 4>(a, st);
+        else
+            launch_tiles<TILE_MODE, OT, true, false, 2, 2, 2, 2, 2>(a, st);
+    } else if constexpr (TILE_MODE == F8X) {
+        if (rows < 128)
+            launch_tiles<F8X, OT, true, true, 3, 2, 4, 2, 2>(a, st);
+        else
+            launch_tiles<F8X, OT, true, true, 3, 2, 4, 4, 4>(a, st);
+    } else {
+        if (rows < (TILE_MODE == BF16 ? 64 : 24) || a.E * ceil_div(rows, 256) * ceil_div(a.N, 256) < CUS)
+            launch_tiles<TILE_MODE, OT, true, true, 3, 2, 4, 2, 2>(a, st);
+        else
+            launch_groups<TILE_MODE, OT, true>(a, st);
+    }
 }
 
 static moe_status check_product(int32_t N, int32_t n_max, int32_t K, int32_t out_dtype)
@@ -839,6 +1059,8 @@ extern "C" moe_status moe_linear_fp8(const void *q, int64_t ldq, const float *s,
     const int64_t blocks = (K + 127) / 128;
     if (ldq < K || ldw < K || ldo < N || lds < blocks || ldws < blocks)
         return fail(MOE_E_INVAL, "a leading dimension is below its row's length");
+    if (lds > (1 << 21))                             // a tile's scales are within 2^31 bytes
+        return fail(MOE_E_INVAL, "lds=%lld above 2^21", (long long)lds);
     if (!ops_aligned(s, 4) || !ops_aligned(ws, 4) || !ops_aligned(bias, 4) ||
         !ops_aligned(out, out_dtype == MOE_DT_F32 ? 4 : 2))
         return fail(MOE_E_INVAL, "s, ws, bias and out must be aligned to their elements");
@@ -846,7 +1068,10 @@ extern "C" moe_status moe_linear_fp8(const void *q, int64_t ldq, const float *s,
         return st;
     const ProdArgs a{static_cast<const uint8_t *>(q), static_cast<const uint8_t *>(w), s, ws, bias, out,
                      nullptr, nullptr, ldq, ldw, 0, lds, ldws, 0, ldo, T, T, N, 1, K};
-    enqueue_f8<false>(a, out_dtype, static_cast<hipStream_t>(stream));
+    if (out_dtype == MOE_DT_F32)
+        enqueue_dense<F8X, F8X, float>(a, static_cast<hipStream_t>(stream));
+    else
+        enqueue_dense<F8X, F8, bf16_t>(a, static_cast<hipStream_t>(stream));
     return launched("E4M3 product launch");
 }
 
@@ -878,6 +1103,8 @@ extern "C" moe_status moe_grouped_linear(const void *x, int32_t x_dtype, int64_t
     const int64_t blocks = (K + 127) / 128, nblocks = (N + 127) / 128;
     if (ldx < K || ldw < K || ldo < N || (f8 && (lds < blocks || ldws < blocks)))
         return fail(MOE_E_INVAL, "a leading dimension is below its row's length");
+    if (f8 && (rows ? R * lds > (1 << 29) : lds > (1 << 21)))   // a tile's scales are within 2^31 bytes
+        return fail(MOE_E_INVAL, "lds=%lld too large", (long long)lds);
     if (E > 1 && (w_stride < (int64_t)(N - 1) * ldw + K || (f8 && ws_stride < (nblocks - 1) * ldws + blocks)))
         return fail(MOE_E_INVAL, "w_stride or ws_stride is below an expert's size");
     if (!ops_aligned(rows, 4) || !ops_aligned(offsets, 4) || (f8 && (!ops_aligned(s, 4) || !ops_aligned(ws, 4))) ||
@@ -890,11 +1117,13 @@ extern "C" moe_status moe_grouped_linear(const void *x, int32_t x_dtype, int64_t
                      rows, offsets, ldx * b, ldw * b, w_stride * b, lds, ldws, ws_stride, ldo, R, M, N, E,
                      (int)(K * b)};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (f8)
-        enqueue_f8<true>(a, out_dtype, hs);
+    if (f8 && out_dtype == MOE_DT_F32)
+        enqueue_grouped<F8X, F8X, float>(a, hs);
+    else if (f8)
+        enqueue_grouped<F8X, F8, bf16_t>(a, hs);
     else if (out_dtype == MOE_DT_F32)
-        enqueue_product<BF16, BF16, float, true>(a, hs);
+        enqueue_grouped<BF16, BF16, float>(a, hs);
     else
-        enqueue_product<BF16, BF16, bf16_t, true>(a, hs);
+        enqueue_grouped<BF16, BF16, bf16_t>(a, hs);
     return launched("grouped product launch");
 }

@@ -113,6 +113,15 @@ def limit(x, w, size, out_bf16, unit_fp8):
     return lim + 1e-37
 
 
+def some_rows(n, first=0):
+    """Up to some 40 of n rows: those around the tiles' borders, and a few between."""
+    if n <= 40:
+        return np.arange(first, first + n)
+    edges = [r + d for r in (0, 16, 32, 64, 128, 192, 256, n) for d in (-1, 0)] + [r for r in (n // 3, n // 2, n - 17, n - 33)]
+    edges += list(range(0, n, max(1, n // 16)))
+    return first + np.unique([r for r in edges if 0 <= r < n])
+
+
 def group(idx, E):
     """offsets, rows, pos of ids [T,k]."""
     flat = np.asarray(idx).reshape(-1)

@@ -164,9 +164,10 @@ def linear_inputs(seed, T, N, K):
 
 
 def check_linear(y, q, s, w, ws, bias, out):
-    x, v = ref.scaled(q, s), ref.scaled_weights(w, ws)
+    at = ref.some_rows(q.shape[0])
+    y, x, v = y[at], ref.scaled(q[at], s[at]), ref.scaled_weights(w, ws)
     want = x @ v.T
-    lim = ref.limit(x, v, 1, out == "bf16", out == "bf16")
+    lim = ref.limit(x, v, 1, out == "bf16", out == "bf16" and q.shape[0] > 32)
     if bias is not None:
         want = want + bias
         lim = lim + (2 * U + (2.0 ** -8 if out == "bf16" else 0)) * np.abs(bias)
@@ -184,6 +185,25 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (2, 33, 64), (3, 130, 129), (8, 257, 1000), (
 def test_linear_sizes(out, T, N, K):
     q, s, w, ws, bias = linear_inputs(5, T, N, K)
     check_linear(run_linear(q, s, w, ws, None, out), q, s, w, ws, None, out)
+
+
+# Shapes whose rounds over the CUs cost least as tiles of 64x64, 64x128, 128x128, 128x256 and 256x256
+# (fp32 outputs: up to 128x256); rows on 16 bytes, on 4, and on single ones (through registers).
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N", [(64, 6100), (320, 5003), (512, 5000), (1100, 4600), (2100, 4700)])
+@pytest.mark.parametrize("K,pad,shift", [(256, 0, 0), (520, 8, 8), (1300, 4, 4), (300, 3, 1), (100, 4, 0)])
+def test_linear_tiles(out, T, N, K, pad, shift):
+    q, s, w, ws, bias = linear_inputs(10, T, N, K)
+    check_linear(run_linear(q, s, w, ws, bias, out, pad, shift, pad), q, s, w, ws, bias, out)
+
+
+def test_linear_tiles_give_the_same_bits_in_every_shape():
+    """Blocks' sums are added in their order whatever the tile: rows of a large product equal those of
+    a smaller one."""
+    q, s, w, ws, _ = linear_inputs(11, 2100, 4700, 1000)
+    y = run_linear(q, s, w, ws, None, "bf16")
+    for T in (512, 1100):
+        assert np.array_equal(run_linear(q[:T], s[:T], w, ws, None, "bf16"), y[:T])
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])

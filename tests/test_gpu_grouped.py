@@ -116,14 +116,15 @@ class Inputs:
 
     def check(self, y, out):
         o = self.offsets
+        unit_fp8 = self.xd == "fp8" and out == "bf16" and self.M > 12 * self.E
         assert (y[:self.lead] == CANARY).all() and (y[o[-1]:] == CANARY).all()
         for e in range(self.E):
             if o[e] == o[e + 1]:
                 continue
-            x = self.xv[self.rows[o[e]:o[e + 1]] if self.rows is not None else slice(o[e], o[e + 1])]
-            f8 = self.xd == "fp8"
-            lim = ref.limit(x, self.wv[e], 1 if f8 else 2, out == "bf16", f8 and out == "bf16")
-            off = np.abs(y[o[e]:o[e + 1]] - x @ self.wv[e].T)
+            at = ref.some_rows(o[e + 1] - o[e], o[e])
+            x = self.xv[self.rows[at] if self.rows is not None else at]
+            lim = ref.limit(x, self.wv[e], 1 if self.xd == "fp8" else 2, out == "bf16", unit_fp8)
+            off = np.abs(y[at] - x @ self.wv[e].T)
             assert (off <= lim).all(), (e, float((off - lim).max()))
 
 
@@ -140,6 +141,25 @@ MANY = [70, 0, 129, 1, 64, 200, 65]
 def test_grouped_sizes(xd, out, gather, sizes, N, K):
     c = Inputs(1, sizes, N, K, xd, gather)
     c.check(c.run(out), out)
+
+
+# groups of every size up to more than a tile's 256 rows, of so many channels that the tiles are 256 wide (E4M3 to
+# fp32: 128 x 256); rows on 16 bytes, on 4, and on single ones
+@pytest.mark.parametrize("xd", ["fp8", "bf16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("K,pad,shift", [(256, 0, 0), (1100, 4, 4), (200, 3, 1), (60, 4, 0)])
+@pytest.mark.parametrize("mean", [30, 140])
+def test_grouped_tiles(xd, out, K, pad, shift, mean):
+    sizes = {30: [64, 0, 1, 65, 130, 10, 5, 3], 140: [64, 0, 128, 129, 192, 193, 256, 300, 1]}[mean] * 4
+    c = Inputs(8, sizes, 2600, K, xd, mean == 30)
+    c.check(c.run(out, pad, shift, pad), out)
+
+
+# a few rows to an expert, with weights so many that they are read past the cache
+@pytest.mark.parametrize("sizes", [[1, 0, 3, 2] * 8, [9, 0, 17, 5] * 8])
+def test_grouped_streams_of_many_weights(sizes):
+    c = Inputs(9, sizes, 4000, 4200, "fp8", True)
+    c.check(c.run("bf16"), "bf16")
 
 
 @pytest.mark.parametrize("xd", ["fp8", "bf16"])

@@ -9,7 +9,17 @@ RMS norm that takes the residual's addition.
     MoEFFN.forward:    moe_rmsnorm_quant -> moe_router_topk_grouped ->
                        moe_expert_ffn
 
-Both take the last half's output and the residual stream and give their own
+and the same two with E4M3 weights (a scale for each block of 128 x 128):
+
+    Fp8DenseFFN.forward:  moe_rmsnorm_quant -> moe_quant_fp8 -> moe_linear_fp8 ->
+                          moe_quant_fp8 (SwiGLU) -> moe_linear_fp8
+    Fp8MoEFFN.forward:    moe_rmsnorm_quant -> moe_grouped_linear (the router's
+                          logits) -> moe_route_select -> moe_group_rows ->
+                          moe_quant_fp8 -> moe_grouped_linear -> moe_quant_fp8
+                          (SwiGLU) -> moe_grouped_linear -> moe_combine_rows, on
+                          top of the shared expert's two moe_linear_fp8
+
+All take the last half's output and the residual stream and give their own
 output and the new stream, so halves follow one another:
 
     y, res = dense.forward(attn_out, res)
@@ -54,6 +64,41 @@ def quantise_weight(w):
     q = torch.clamp(torch.round((w * pre[:, None]) * inv[:, None]), -127, 127)
     q = torch.where(fine[:, None], q, 0.0).to(torch.int8)
     return q.contiguous(), torch.where(fine, amax / 127.0, float("nan"))
+
+
+def quantise_weight_fp8(w):
+    """E4M3 codes [.., N, K] (torch.float8_e4m3fn) and scales [.., ceil(N/128), ceil(K/128)]
+    of weights, by the rule of the activations (moe_quant_fp8) for each block of
+    128 x 128: a zero block gets scale 0, one with a NaN or an infinity scale NaN and
+    codes 0."""
+    import torch
+    N, K = w.shape[-2:]
+    nb, kb = -(-N // 128), -(-K // 128)
+    by = torch.nn.functional.pad(w.float(), (0, 128 * kb - K, 0, 128 * nb - N)).unflatten(-1, (kb, 128)).unflatten(-3, (nb, 128))
+    amax = by.abs().amax(dim=(-1, -3))
+    fine = torch.isfinite(amax)
+    pre = torch.ones_like(amax).masked_fill(amax < 2.0 ** -96, 2.0 ** 64)
+    inv = torch.where(fine & (amax > 0), 448.0 / (amax * pre), 0.0)
+    at = lambda v: v[..., :, None, :, None]  # noqa: E731
+    q = torch.where(at(fine), (by * at(pre)) * at(inv), 0.0).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    q = q.flatten(-4, -3).flatten(-2, -1)[..., :N, :K]
+    return q.contiguous(), torch.where(fine, amax / 448.0, float("nan"))
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _fp8_weights(t, w, s, shape, name):
+    """Checks E4M3 weights of a shape and their scales, and returns both as they are read."""
+    if w.dtype != t.float8_e4m3fn:
+        raise ValueError("%s must be E4M3 codes (torch.float8_e4m3fn), not %s" % (name, w.dtype))
+    if tuple(w.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(w.shape), tuple(shape)))
+    want = tuple(shape[:-2]) + (_blocks(shape[-2]), _blocks(shape[-1]))
+    if tuple(s.shape) != want:
+        raise ValueError("the scales of %s have shape %s, expected %s" % (name, tuple(s.shape), want))
+    return w.contiguous(), s.float().contiguous()
 
 
 class _Norm:
@@ -206,4 +251,124 @@ class MoEFFN(_Norm):
             abi.moe_router_topk_grouped(self.layer.ctx, self.route, self.y, T, self.layer.weights, self.idx,
                                         self.w, stream)
             abi.moe_expert_ffn(self.layer.ctx, self.y, T, self.layer.weights, self.idx, self.w, out, stream)
+        return out, h
+
+
+class Fp8DenseFFN(_Norm):
+    """A dense SwiGLU FFN with E4M3 weights: gate_up [2F, H] (the gate rows above the
+    up rows) with scales s_gu [ceil(2F/128), ceil(H/128)], down [H, F] with s_dn
+    [ceil(H/128), ceil(F/128)] (quantise_weight_fp8 makes them)."""
+
+    def __init__(self, gamma, gate_up, s_gu, down, s_dn, max_tokens, eps=1e-6, out_dtype=None):
+        super().__init__(gamma, max_tokens, eps)
+        t, H = self.torch, self.H
+        if gate_up.dim() != 2 or down.dim() != 2:
+            raise ValueError("gate_up and down must be matrices")
+        F = self.F = down.shape[1]
+        self.gate_up, self.s_gu = _fp8_weights(t, gate_up, s_gu, (2 * F, H), "gate_up")
+        self.down, self.s_dn = _fp8_weights(t, down, s_dn, (H, F), "down")
+        if any(a.device != self.dev for a in (self.gate_up, self.down, self.s_gu, self.s_dn)):
+            raise ValueError("weights and gamma must be on one device")
+        self.out_dtype = out_dtype or t.bfloat16
+        if self.out_dtype not in (t.float32, t.bfloat16):
+            raise ValueError("out_dtype must be fp32 or bf16, not %s" % self.out_dtype)
+        n = self.max_tokens
+        e = lambda *shape, dt: t.empty(shape, dtype=dt, device=self.dev)  # noqa: E731
+        self.y, self.gu = e(n, H, dt=t.bfloat16), e(n, 2 * F, dt=t.bfloat16)
+        self.q, self.s = e(n, H, dt=t.float8_e4m3fn), e(n, _blocks(H), dt=t.float32)
+        self.qh, self.sh = e(n, F, dt=t.float8_e4m3fn), e(n, _blocks(F), dt=t.float32)
+        self._made()
+
+    def forward(self, x, residual, stream=None):
+        """As DenseFFN.forward."""
+        H, F = self.H, self.F
+        rows = self._check(x, residual)
+        with self._on(stream, x, residual):
+            T, h = self._norm(x, residual, rows, self.y, None, None, stream)
+            out = self.torch.empty((T, H), dtype=self.out_dtype, device=self.dev)
+            abi.moe_quant_fp8(self.y, abi.DT_BF16, H, abi.ACT_NONE, T, H, None, self.q, H, self.s, _blocks(H), stream)
+            _fp8_ffn(self, T, self.q, self.s, out, stream)
+        return out, h
+
+
+def _fp8_ffn(w, T, q, s, out, stream):
+    """The two products of an E4M3 FFN and what is between, for codes q [T, H] with scales s."""
+    H, F = w.H, w.F
+    abi.moe_linear_fp8(q, H, s, _blocks(H), T, w.gate_up, H, w.s_gu, _blocks(H), None, 2 * F, H, w.gu, abi.DT_BF16, 2 * F,
+                       stream)
+    abi.moe_quant_fp8(w.gu, abi.DT_BF16, 2 * F, abi.ACT_SWIGLU, T, F, None, w.qh, F, w.sh, _blocks(F), stream)
+    abi.moe_linear_fp8(w.qh, F, w.sh, _blocks(F), T, w.down, F, w.s_dn, _blocks(F), None, H, F, out, _dtype(out), H, stream)
+
+
+class Fp8MoEFFN(_Norm):
+    """A routed FFN half with E4M3 experts: the norm, the router's logits from router
+    [E, H] (bf16), the choice of experts by `route` (a moe_route_desc) with bias [E] or
+    None, and the experts gate_up [E, 2F, H] with s_gu [E, ceil(2F/128), ceil(H/128)],
+    down [E, H, F] with s_dn [E, ceil(H/128), ceil(F/128)].  `shared`: None, or (gate_up,
+    s_gu, down, s_dn) of an expert that every token takes, of any F."""
+
+    def __init__(self, gamma, router, bias, gate_up, s_gu, down, s_dn, route, max_tokens, shared=None, eps=1e-6,
+                 out_dtype=None):
+        super().__init__(gamma, max_tokens, eps)
+        t, H = self.torch, self.H
+        E, k = route.n_experts, route.top_k
+        if gate_up.dim() != 3 or down.dim() != 3:
+            raise ValueError("gate_up and down must be stacks of the experts' matrices")
+        F = self.F = down.shape[2]
+        self.gate_up, self.s_gu = _fp8_weights(t, gate_up, s_gu, (E, 2 * F, H), "gate_up")
+        self.down, self.s_dn = _fp8_weights(t, down, s_dn, (E, H, F), "down")
+        if tuple(router.shape) != (E, H) or router.dtype != t.bfloat16:
+            raise ValueError("router must be bf16 [%d, %d]" % (E, H))
+        if bias is not None and tuple(bias.shape) != (E,):
+            raise ValueError("bias must have a value for each expert")
+        self.router = router.contiguous()
+        self.bias = None if bias is None else bias.float().contiguous()
+        own = [self.gate_up, self.s_gu, self.down, self.s_dn, self.router] + ([] if bias is None else [self.bias])
+        if any(a.device != self.dev for a in own):
+            raise ValueError("weights and gamma must be on one device")
+        self.out_dtype = out_dtype or t.bfloat16
+        if self.out_dtype not in (t.float32, t.bfloat16):
+            raise ValueError("out_dtype must be fp32 or bf16, not %s" % self.out_dtype)
+        self.route = route
+        self.shared = None
+        if shared is not None:
+            self.shared = Fp8DenseFFN(self.gamma, *shared, max_tokens=max_tokens, eps=eps, out_dtype=self.out_dtype)
+        n, m = self.max_tokens, self.max_tokens * k
+        e = lambda *shape, dt: t.empty(shape, dtype=dt, device=self.dev)  # noqa: E731
+        self.y, self.logits = e(n, H, dt=t.bfloat16), e(n, E, dt=t.float32)
+        self.idx, self.w = e(n, k, dt=t.int32), e(n, k, dt=t.float32)
+        # one group of all rows: its end is taken as their number
+        self.whole = t.tensor([0, 2 ** 31 - 1], dtype=t.int32, device=self.dev)
+        self.offsets, self.rows, self.pos = e(E + 1, dt=t.int32), e(m, dt=t.int32), e(m, dt=t.int32)
+        self.q, self.s = e(n, H, dt=t.float8_e4m3fn), e(n, _blocks(H), dt=t.float32)
+        self.gu, self.yr = e(m, 2 * F, dt=t.bfloat16), e(m, H, dt=t.bfloat16)
+        self.qh, self.sh = e(m, F, dt=t.float8_e4m3fn), e(m, _blocks(F), dt=t.float32)
+        self._made()
+        if self.shared is not None:
+            self._own += self.shared._own
+
+    def forward(self, x, residual, stream=None):
+        """As DenseFFN.forward; the chosen experts and their weights are in idx[:T] and
+        w[:T] afterwards."""
+        H, F, E, k = self.H, self.F, self.route.n_experts, self.route.top_k
+        hb, fb = _blocks(H), _blocks(F)
+        rows = self._check(x, residual)
+        with self._on(stream, x, residual):
+            T, h = self._norm(x, residual, rows, self.y, None, None, stream)
+            M = T * k
+            out = self.torch.empty((T, H), dtype=self.out_dtype, device=self.dev)
+            abi.moe_grouped_linear(self.y, abi.DT_BF16, H, None, 0, T, None, self.whole, 1, T, self.router, H, E * H, None, 0, 0,
+                                   E, H, self.logits, abi.DT_F32, E, stream)
+            abi.moe_route_select(self.route, self.logits, abi.DT_F32, E, self.bias, T, self.idx, self.w, stream)
+            abi.moe_group_rows(self.idx, T, k, E, self.offsets, self.rows, self.pos, stream)
+            abi.moe_quant_fp8(self.y, abi.DT_BF16, H, abi.ACT_NONE, T, H, None, self.q, H, self.s, hb, stream)
+            abi.moe_grouped_linear(self.q, abi.DT_FP8, H, self.s, hb, T, self.rows, self.offsets, E, M, self.gate_up, H,
+                                   2 * F * H, self.s_gu, hb, _blocks(2 * F) * hb, 2 * F, H, self.gu, abi.DT_BF16, 2 * F, stream)
+            abi.moe_quant_fp8(self.gu, abi.DT_BF16, 2 * F, abi.ACT_SWIGLU, M, F, self.offsets[E:], self.qh, F, self.sh, fb, stream)
+            abi.moe_grouped_linear(self.qh, abi.DT_FP8, F, self.sh, fb, M, None, self.offsets, E, M, self.down, F, H * F,
+                                   self.s_dn, fb, hb * fb, H, F, self.yr, abi.DT_BF16, H, stream)
+            if self.shared is not None:
+                _fp8_ffn(self.shared, T, self.q, self.s, out, stream)
+            abi.moe_combine_rows(self.yr, abi.DT_BF16, H, M, self.pos, self.w, out if self.shared is not None else None, H, T, k, H,
+                                 out, _dtype(out), H, stream)
         return out, h

@@ -13,41 +13,56 @@ struct GroupArgs {
 
 // ---------------------------------------------------------------------------
 // Grouping up to 65536 ids in one launch without a workspace: a block per expert
-// reads all ids and counts those below its own (its offset) and its own.  Wave w
-// has a run of neighbouring ids, 64 at a time; the ballots of its own ids stay in
-// the lanes (lane i those of round i), so the second step touches only them: a
-// lane's ids follow those of the lanes, waves and ids before it.
+// reads all ids, counts those below its own (its offset) and lists its own.  Wave w
+// has a run of neighbouring ids, 64 at a time, so its list follows those of the
+// waves before it.  Bound by the instructions of all blocks' rounds (E*M/64 in all):
+// two comparisons each, no bounds in whole batches, more only where an id is found.
 // ---------------------------------------------------------------------------
 constexpr int GROUP_W = 16;                          // waves
 constexpr int GROUP_ONE = 64 * 64 * GROUP_W;         // ids of one launch
 
+// BATCH: rounds whose loads are in flight at once; ROUNDS: of a wave at most
+template <int BATCH, int ROUNDS>
 __global__ __launch_bounds__(64 * GROUP_W) void group_rows_kernel(GroupArgs a)
 {
     __shared__ int below[GROUP_W], own[GROUP_W];
+    __shared__ uint16_t found[GROUP_W][64 * ROUNDS]; // places in the wave's run
     const int lane = threadIdx.x & 63, e = blockIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rounds = (a.M + 64 * GROUP_W - 1) / (64 * GROUP_W), first = wave * rounds * 64;
+    // an id that is no expert has no row: each block looks for them among its share
+    for (int i = (int)((int64_t)a.M * e / a.E) + (int)threadIdx.x; i < (int)((int64_t)a.M * (e + 1) / a.E); i += 64 * GROUP_W)
+        if ((unsigned)a.idx[i] >= (unsigned)a.E)
+            a.pos[i] = -1;
     int nb = 0, no = 0;
-    unsigned long long mask = 0;                     // lane i: this expert's ids of round i
-    for (int r0 = 0; r0 < rounds; r0 += 8) {
-        int id[8];
+    auto count = [&](const int (&id)[BATCH], int r0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < BATCH; ++j) {
+            const unsigned long long m = __ballot(id[j] == e);
+            nb += __popcll(__ballot((unsigned)id[j] < (unsigned)e));
+            if (m) {
+                if (id[j] == e)
+                    found[wave][no + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(64 * (r0 + j) + lane);
+                no += __popcll(m);
+            }
+        }
+    };
+    int r0 = 0;
+    for (; r0 + BATCH <= rounds && first + 64 * (r0 + BATCH) <= a.M; r0 += BATCH) {
+        int id[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            id[j] = a.idx[first + 64 * r0 + lane + 64 * j];
+        count(id, r0);
+    }
+    for (; r0 < rounds && first + 64 * r0 < a.M; r0 += BATCH) {   // the last ids
+        int id[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
             const int i = first + 64 * (r0 + j) + lane;
             id[j] = (r0 + j < rounds && i < a.M) ? a.idx[i] : INT_MAX;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const unsigned long long m = __ballot(id[j] == e);
-            nb += __popcll(__ballot((unsigned)id[j] < (unsigned)e));
-            no += __popcll(m);
-            if (lane == r0 + j)
-                mask = m;
-            // an id that is no expert has no row
-            const int i = first + 64 * (r0 + j) + lane;
-            if (e == 0 && (unsigned)id[j] >= (unsigned)a.E && r0 + j < rounds && i < a.M)
-                a.pos[i] = -1;
-        }
+        count(id, r0);
     }
     if (lane == 0) {
         below[wave] = nb;
@@ -66,16 +81,10 @@ __global__ __launch_bounds__(64 * GROUP_W) void group_rows_kernel(GroupArgs a)
         if (e == a.E - 1)
             a.offsets[a.E] = base + total;
     }
-    int n = __popcll(mask), incl = n;
-#define STEP(c, r) incl += dpp0<c, r>(incl);
-    MOE_DPP_STEPS(STEP)
-#undef STEP
-    int g = base + at + incl - n;
-    for (; mask; mask &= mask - 1) {
-        const int i = first + 64 * lane + __ffsll(mask) - 1;
+    for (int n = lane; n < no; n += 64) {
+        const int i = first + found[wave][n], g = base + at + n;
         a.rows[g] = i / a.k;
         a.pos[i] = g;
-        ++g;
     }
 }
 
@@ -199,7 +208,7 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int runs
 
 // ---------------------------------------------------------------------------
 // out[t] = base[t] + sum_i w[t,i] * y[pos[t,i]], fp32 FMAs in the order of i,
-// rounded once.  A thread has eight columns of a token; the loads of four of
+// rounded once.  A thread has eight columns of a token; the loads of eight of
 // its rows are in flight at once.
 // ---------------------------------------------------------------------------
 struct CombineArgs {
@@ -235,12 +244,12 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a)
             for (int j = 0; j < 8; ++j)
                 v[j] = 0.0f;
         }
-        for (int i0 = 0; i0 < a.k; i0 += 4) {
-            raw8<YT> r[4];
-            float wi[4];
-            bool in[4];
+        for (int i0 = 0; i0 < a.k; i0 += 8) {
+            raw8<YT> r[8];
+            float wi[8];
+            bool in[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const int p = (i0 + i < a.k) ? pos[i0 + i] : -1;
                 in[i] = (unsigned)p < (unsigned)a.R;
                 wi[i] = in[i] ? w[i0 + i] : 0.0f;
@@ -248,7 +257,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a)
                     r[i].load(y + (int64_t)p * a.ldy);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 if (in[i]) {
                     float x[8];
                     r[i].widen(x);
@@ -301,7 +310,12 @@ extern "C" moe_status moe_group_rows(const int32_t *idx, int32_t T, int32_t k, i
     const GroupArgs a{idx, offsets, rows, pos, T * k, k, E};
     hipStream_t hs = static_cast<hipStream_t>(stream);
     if (a.M <= GROUP_ONE) {
-        launch(group_rows_kernel, (unsigned)E, 64 * GROUP_W, 0, hs, a);
+        if (a.M <= 4 * 64 * GROUP_W)
+            launch(group_rows_kernel<4, 4>, (unsigned)E, 64 * GROUP_W, 0, hs, a);
+        else if (a.M <= 16 * 64 * GROUP_W)
+            launch(group_rows_kernel<8, 16>, (unsigned)E, 64 * GROUP_W, 0, hs, a);
+        else
+            launch(group_rows_kernel<16, 64>, (unsigned)E, 64 * GROUP_W, 0, hs, a);
     } else {
         const int runs = a.M / GROUP_RUN;
         launch(group_count_kernel, (unsigned)runs, 1024, 0, hs, a, runs);

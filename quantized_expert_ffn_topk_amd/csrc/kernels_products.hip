@@ -487,8 +487,8 @@ __global__ __launch_bounds__(64 * W, 2) void product_stream_kernel(ProdArgs a, i
 // reads of one piece fall on different banks.
 // DMA: rows go global -> LDS by the load unit (a wave's copy is 8 rows, lane l
 // writing slot l%8 of row l/8, so the lane picks the global piece that belongs
-// there); needs rows of 16-byte alignment, not too far apart.  Otherwise they pass
-// through registers.  The last, partial stage always does (load_piece_end's zeros).
+// there); needs rows on 4 bytes, not too far apart.  Otherwise they pass through
+// registers.
 // Scales: the weights' of all stages lie in LDS from the beginning, the rows'
 // come four stages at a time (16 bytes of a row of scales; one by one they would
 // be a line each) into one of two places while the other is read.
@@ -535,7 +535,7 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lds0 = (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-    const int stages = a.K >> 7, blocks = (a.K + 127) >> 7;
+    const int stages = (a.K + 127) >> 7;             // the last may be partial
     const bool gathered = GROUPED && a.rows;
 
     // copies
@@ -548,6 +548,9 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     auto lds_at = [&](int i) INLINE { return (i < TP ? 0 : BT * 128) + 1024 * (wave + NW * (i < TP ? i : i - TP)); };
     const uint8_t *x0 = uniform(gathered ? a.x : a.x + (int64_t)t.row0 * a.ldx);
     const uint8_t *w0 = uniform(t.w + (int64_t)t.n0 * a.ldw);
+    // the ends of the last rows: past them copies bring zeros
+    const uint32_t x_end = (uint32_t)(((gathered ? a.R : t.rows) - 1) * a.ldx + a.K);
+    const uint32_t w_end = (uint32_t)((min(S::BN, a.N - t.n0) - 1) * a.ldw + a.K);
     uint32_t lane_at[DMA ? CP : 1];                  // this lane's piece of each copy
     const uint8_t *src[DMA ? 1 : CP];
 #pragma unroll
@@ -560,7 +563,10 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     v4i reg[DMA ? 1 : CP];
     auto fetch = [&](int i, int buf, int st) INLINE {    // sets out copy i of stage st
         if constexpr (DMA)
-            copy16(buffer_of(i < TP ? x0 : w0, st < stages ? 0xffffffffu : 0u), lane_at[i], 128 * st, lds0 + buf + lds_at(i));
+            copy16(buffer_of(i < TP ? x0 : w0, st < stages ? (i < TP ? x_end : w_end) : 0u), lane_at[i], 128 * st,
+                   lds0 + buf + lds_at(i));
+        else if ((a.K & 127) && st >= stages - 1)
+            reg[i] = load_piece_end(src[i] - 16 * piece, 128 * (stages - 1) + 16 * piece, a.K);
         else
             reg[i] = load_piece(src[i] + 128 * min(st, stages - 1));
     };
@@ -569,6 +575,18 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
 #pragma unroll
             for (int i = 0; i < CP; ++i)
                 *reinterpret_cast<v4i *>(lds + buf + lds_at(i) + 16 * lane) = reg[i];
+        }
+    };
+    // a row's partial last stage has, past the row's end, what lies behind it: zeros take its place
+    auto clean = [&](int buf) INLINE {
+        const int kept = a.K & 127, np = 8 - (kept >> 4);
+        for (int f = tid; f < (BT + S::BN) * np; f += 64 * NW) {
+            const int row = f / np, c = (kept >> 4) + f - row * np;
+            v4i *at = reinterpret_cast<v4i *>(lds + buf + 128 * row + 16 * (c ^ ((row >> 1) & 7)));
+            unsigned __int128 v = 0;
+            if (16 * c < kept)
+                v = __builtin_bit_cast(unsigned __int128, *at) & (((unsigned __int128)1 << (8 * (kept & 15))) - 1);
+            *at = __builtin_bit_cast(v4i, v);
         }
     };
 
@@ -580,15 +598,15 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
         const int r = min(64 * wave + lane, t.rows - 1);
         s_lane = (uint32_t)((gathered ? source_row<GROUPED>(a, t.row0 + r) : r) * a.lds * 4);
         // its end is the last row's: what a quad has past it reads as 0
-        s_rows = buffer_of(uniform(s0), (uint32_t)(((int64_t)((gathered ? a.R : t.rows) - 1) * a.lds + blocks) * 4));
-        for (int i = wave; i < S::WB * ((blocks + 63) >> 6); i += NW) {
+        s_rows = buffer_of(uniform(s0), (uint32_t)(((int64_t)((gathered ? a.R : t.rows) - 1) * a.lds + stages) * 4));
+        for (int i = wave; i < S::WB * ((stages + 63) >> 6); i += NW) {
             const int b = i % S::WB, k = i / S::WB * 64;
             const float *row = t.ws + (int64_t)(min(t.n0 + 128 * b, a.N - 1) >> 7) * a.ldws;
-            copy4(row + min(k + lane, blocks - 1), lds0 + S::WSCALE + 4 * (b * MAX_BLOCKS + k));
+            copy4(row + min(k + lane, stages - 1), lds0 + S::WSCALE + 4 * (b * MAX_BLOCKS + k));
         }
     }
     auto bring = [&](int q) INLINE {                 // sets out a quad's copy
-        if (SCALED && 64 * wave < BT && 4 * q < blocks)
+        if (SCALED && 64 * wave < BT && 4 * q < stages)
             copy16(s_rows, s_lane, 16 * q, lds0 + S::TSCALE + 16 * (SROWS * (q & 1) + 64 * wave));
     };
 
@@ -664,16 +682,24 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
             asm volatile("" : "+v"(acc[i][j]));
         }
     };
-    // stage st, whose rows are in cur; LAST: none is read ahead
-    auto run_stage = [&](auto last_, int cur, int next, int st) INLINE {
-        constexpr bool LAST = decltype(last_)::value;
+    auto meet_clean = [&](int buf) INLINE {
+        clean(buf);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xc07f);          // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // stage st, whose rows are in cur
+    auto run_stage = [&](int cur, int next, int st) INLINE {
         ws = ws_next;
         steps_of<FT>([&](auto i_) INLINE {
             constexpr int i = decltype(i_)::value;
             sc[i & 1] = sv[i % XR] * ws;
-            if constexpr (i == TURN && !LAST) {
+            if constexpr (i == TURN) {
                 land(next);
                 meet(std::integral_constant<int, NB - 2>());
+                if (DMA && (a.K & 127) && st + 2 == stages)
+                    meet_clean(next);
                 if (SCALED && (st & 3) == 3)         // its quad's place is free
                     bring((st >> 2) + 2);
                 scales_of(st + 1);
@@ -681,7 +707,7 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
             if constexpr (i < TURN) {
                 read_x(xf[(i + LA) % XR], cur, i + LA);
                 read_s(i + LA);
-            } else if constexpr (!LAST) {
+            } else {
                 read_x(xf[(i + LA) % XR], next, i + LA - FT);
                 read_s(i + LA - FT);
             }
@@ -693,7 +719,7 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
                 } else {
                     acc[i][j] = stage_product<MODE>(wf[j], xf[i % XR], acc[i][j]);
                 }
-                if constexpr (i >= TURN && !LAST) {
+                if constexpr (i >= TURN) {
 #pragma unroll
                     for (int c = slot * CP / SLOTS; c < (slot + 1) * CP / SLOTS; ++c)
                         fetch(c, cur, st + NB);
@@ -715,40 +741,26 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
         for (int j = 0; j < FN; ++j)
             read_w(wf[j], buf, j);
     };
-    const std::false_type more;
-    const std::true_type last;
     bring(0);
     bring(1);
-    if (stages > 0) {
-        // registers hold one stage, so that there is one less on its way
+    // registers hold one stage, so that there is one less on its way
 #pragma unroll
-        for (int b = 0; b < (DMA ? NB : 2); ++b) {
-#pragma unroll
-            for (int i = 0; i < CP; ++i)
-                fetch(i, b * BUF, b);
-            if (b == 0)
-                land(0);
-        }
-        meet(std::integral_constant<int, NB - 1>());
-        begin(0, 0);
-        int cur = 0;
-        for (int st = 0; st < stages; ++st) {
-            const int next = (cur == (NB - 1) * BUF) ? 0 : cur + BUF;
-            run_stage(more, cur, next, st);
-            cur = next;
-        }
-    }
-    if (a.K & 127) {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        const int k = 128 * stages + 16 * piece;
+    for (int b = 0; b < (DMA ? NB : 2); ++b) {
 #pragma unroll
         for (int i = 0; i < CP; ++i)
-            *reinterpret_cast<v4i *>(lds + lds_at(i) + 16 * lane) = load_piece_end(row_of(i), k, a.K);
-        __syncthreads();
-        begin(0, stages);
-        run_stage(last, 0, 0, stages);
+            fetch(i, b * BUF, b);
+        if (b == 0)
+            land(0);
+    }
+    meet(std::integral_constant<int, NB - 1>());
+    if (DMA && a.K < 128)
+        meet_clean(0);
+    begin(0, 0);
+    int cur = 0;
+    for (int st = 0; st < stages; ++st) {
+        const int next = (cur == (NB - 1) * BUF) ? 0 : cur + BUF;
+        run_stage(cur, next, st);
+        cur = next;
     }
     steps_of<LAG>([&](auto j_) INLINE { add(j_, 0.0f, sc[(FT - 1) & 1]); });
     asm volatile("" ::: "memory");

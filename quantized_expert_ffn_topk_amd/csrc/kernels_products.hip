@@ -548,9 +548,10 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     auto lds_at = [&](int i) INLINE { return (i < TP ? 0 : BT * 128) + 1024 * (wave + NW * (i < TP ? i : i - TP)); };
     const uint8_t *x0 = uniform(gathered ? a.x : a.x + (int64_t)t.row0 * a.ldx);
     const uint8_t *w0 = uniform(t.w + (int64_t)t.n0 * a.ldw);
-    // the ends of the last rows: past them copies bring zeros
-    const uint32_t x_end = (uint32_t)(((gathered ? a.R : t.rows) - 1) * a.ldx + a.K);
-    const uint32_t w_end = (uint32_t)((min(S::BN, a.N - t.n0) - 1) * a.ldw + a.K);
+    // the ends of the last rows, past which copies bring zeros, on whole words (a word is
+    // read as 0 unless all of it is inside)
+    const uint32_t x_end = ((uint32_t)(((gathered ? a.R : t.rows) - 1) * a.ldx + a.K) + 3) & ~3u;
+    const uint32_t w_end = ((uint32_t)((min(S::BN, a.N - t.n0) - 1) * a.ldw + a.K) + 3) & ~3u;
     uint32_t lane_at[DMA ? CP : 1];                  // this lane's piece of each copy
     const uint8_t *src[DMA ? 1 : CP];
 #pragma unroll
@@ -1115,7 +1116,7 @@ extern "C" moe_status moe_grouped_linear(const void *x, int32_t x_dtype, int64_t
     const int64_t blocks = (K + 127) / 128, nblocks = (N + 127) / 128;
     if (ldx < K || ldw < K || ldo < N || (f8 && (lds < blocks || ldws < blocks)))
         return fail(MOE_E_INVAL, "a leading dimension is below its row's length");
-    if (f8 && (rows ? R * lds > (1 << 29) : lds > (1 << 21)))   // a tile's scales are within 2^31 bytes
+    if (f8 && (lds > (rows ? (1 << 29) / R : 1 << 21)))   // a tile's scales are within 2^31 bytes
         return fail(MOE_E_INVAL, "lds=%lld too large", (long long)lds);
     if (E > 1 && (w_stride < (int64_t)(N - 1) * ldw + K || (f8 && ws_stride < (nblocks - 1) * ldws + blocks)))
         return fail(MOE_E_INVAL, "w_stride or ws_stride is below an expert's size");

@@ -197,6 +197,15 @@ def test_linear_tiles(out, T, N, K, pad, shift):
     check_linear(run_linear(q, s, w, ws, bias, out, pad, shift, pad), q, s, w, ws, bias, out)
 
 
+# rows on 4 bytes whose length is not of whole words: the last row's last word is partly behind it
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N", [(40, 300), (320, 5003), (512, 5000), (1100, 4600), (2100, 4700)])
+@pytest.mark.parametrize("K,pad", [(513, 3), (1302, 2), (127, 1), (3, 1)])
+def test_linear_rows_that_end_inside_a_word(out, T, N, K, pad):
+    q, s, w, ws, _ = linear_inputs(12, T, N, K)
+    check_linear(run_linear(q, s, w, ws, None, out, pad), q, s, w, ws, None, out)
+
+
 def test_linear_tiles_give_the_same_bits_in_every_shape():
     """Blocks' sums are added in their order whatever the tile: rows of a large product equal those of
     a smaller one."""

@@ -155,6 +155,17 @@ def test_grouped_tiles(xd, out, K, pad, shift, mean):
     c.check(c.run(out, pad, shift, pad), out)
 
 
+# rows on 4 bytes whose length is not of whole words: the last row's last word is partly behind it
+@pytest.mark.parametrize("xd", ["fp8", "bf16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("K,pad", [(515, 1), (127, 1), (3, 1)])
+@pytest.mark.parametrize("N", [66, 2600])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_rows_that_end_inside_a_word(xd, out, K, pad, N, gather):
+    c = Inputs(10, [64, 0, 1, 65, 130, 193, 300, 40] * 3, N, K, xd, gather)
+    c.check(c.run(out, pad), out)
+
+
 # a few rows to an expert, with weights so many that they are read past the cache
 @pytest.mark.parametrize("sizes", [[1, 0, 3, 2] * 8, [9, 0, 17, 5] * 8])
 def test_grouped_streams_of_many_weights(sizes):

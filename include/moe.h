@@ -320,7 +320,8 @@ moe_status moe_router_topk_grouped(moe_ctx *ctx, const moe_route_desc *desc, con
  * What a block needs whose weights come as E4M3 codes with a scale for each block of
  * 128 x 128, as the family's own checkpoints have them, or as bf16 experts.  Like the
  * operators above these calls take no context, allocate nothing, keep nothing, run
- * on the current device and may be captured; the same errors.
+ * on the current device and may be captured; the same errors.  Outputs overlap nothing
+ * that the call reads, but for base below.
  *
  * Codes: E4M3 bytes (OCP; largest 448, 0x7f and 0xff NaN, no infinities).  A row of K
  * codes has ceil(K/128) fp32 scales, one for each block of 128 neighbouring codes (the
@@ -338,8 +339,8 @@ moe_status moe_router_topk_grouped(moe_ctx *ctx, const moe_route_desc *desc, con
  *
  * moe_linear_fp8: out[t,n] = bias[n] + sum_b (sum_{k in b} q[t,k]*w[n,k]) *
  * (s[t,b]*ws[n/128,b]); the sums over blocks in fp32, bias [N] or NULL.  Those of a block
- * are fp32 too where out is MOE_DT_F32, and where rows are few (T up to 32; up to 12 in
- * a group on average); else, for MOE_DT_BF16, they are the E4M3 matrix unit's: it
+ * are fp32 too where out is MOE_DT_F32, and where rows are few (T up to 32 at least; up to
+ * 12 in a group on average); else, for MOE_DT_BF16, they are the E4M3 matrix unit's: it
  * aligns 8 neighbouring products to the largest and drops what lies 2^-13 of that
  * one's power of two below (1.4e-5 of a sum of normal codes; a rounding to bf16 is
  * 2^-8).  T in [0, 2^20], 1 <= N <= 2^20, T*N <= 2^35.

@@ -31,7 +31,7 @@ CASES = {
     "moe_grouped_linear": (GROUPED, [
         dict(x=None), dict(s=None), dict(offsets=None), dict(w=None), dict(ws=None), dict(out=None), dict(x_dtype=0), dict(x_dtype=3),
         dict(R=0), dict(rows=None), dict(E=0), dict(E=1025), dict(M=-1), dict(M=(1 << 25) + 1), dict(N=0), dict(K=0), dict(ldx=199),
-        dict(ldw=199), dict(lds=1), dict(lds=1 << 29), dict(rows=None, R=20, lds=(1 << 21) + 1), dict(ldws=1), dict(ldo=129), dict(w_stride=130 * 200 - 1), dict(ws_stride=3), dict(out_dtype=2),
+        dict(ldw=199), dict(lds=1), dict(lds=1 << 29), dict(R=4, lds=1 << 62), dict(rows=None, R=20, lds=(1 << 21) + 1), dict(ldws=1), dict(ldo=129), dict(w_stride=130 * 200 - 1), dict(ws_stride=3), dict(out_dtype=2),
         dict(rows=P + 2), dict(offsets=P + 1), dict(s=P + 2), dict(ws=P + 2), dict(out=P + 1), dict(x_dtype=1, x=P + 1),
         dict(x_dtype=1, w=P + 1), dict(x_dtype=1, out_dtype=0, out=P + 2),
         dict(N=(1 << 17) + 1, ldo=1 << 18, w_stride=1 << 28, ws_stride=1 << 14),

@@ -7,7 +7,8 @@ import pytest
 from quantized_expert_ffn_topk_amd import abi
 from tests import fp8_ref as ref
 from tests import operators_ref as oref
-from tests.test_gpu_fp8 import CANARY, DEV, DT, TDT, check_canary, dev_rows, np_of, out_rows
+from tests.test_gpu_fp8 import (CANARY, DEV, DT, TDT, check_canary, check_linear, dev_rows, linear_inputs, np_of,
+                                out_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -346,3 +347,73 @@ def test_a_run_through_the_experts(T):
                 assert (np.abs(got[a:b] - v[a:b] @ w.T) <= ref.limit(v[a:b], w, 1, True, True)).all()
     terms = np.where(p[:, :, None] < 0, 0.0, gate[:, :, None].astype(np.float64) * yv[np.maximum(p, 0)])
     assert (np.abs(out.cpu().numpy() - terms.sum(axis=1)) <= k * U * np.abs(terms).sum(axis=1) + 1e-37).all()
+
+
+# ---------------------------------------------------------------------------
+# rows far apart: offsets that pass 32 bits, in bytes and in elements
+# ---------------------------------------------------------------------------
+def far(n, row, dtype, ld, fill=0):
+    """[n, row] on the device, `ld` elements from one to the next."""
+    flat = torch.full(((n - 1) * ld + row,), fill, dtype=dtype, device=DEV)
+    return flat.as_strided((n, row), (ld, 1))
+
+
+def on(view, a):
+    view.copy_(torch.from_numpy(np.ascontiguousarray(a)))
+    return view
+
+
+# distances that copies by the load unit reach (up to 2^23 bytes between rows) and that they do not
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,ld", [(3, (1 << 31) + 4), (600, 1 << 22), (300, (1 << 23) + 4)])
+def test_linear_of_rows_far_apart(out, T, ld):
+    N, K = 150, 300
+    q, s, w, ws, bias = linear_inputs(13, T, N, K)
+    lds, ldo = (1 << 21) if T < 600 else 1 << 20, (1 << 30) + 2 if T == 3 else 1 << 22
+    qt = on(far(T, K, torch.uint8, ld), q)
+    st, wst = on(far(T, 3, torch.float32, lds), s), on(far(2, 3, torch.float32, 1 << 30), ws)
+    wt = on(far(N, K, torch.uint8, ld if T == 600 else 1 << 24), w)
+    y = far(T, N, TDT[out], ldo)
+    torch.cuda.synchronize()
+    abi.moe_linear_fp8(qt, ld, st, lds, T, wt, ld if T == 600 else 1 << 24, wst, 1 << 30, torch.from_numpy(bias).to(DEV), N, K, y,
+                       DT[out], ldo)
+    torch.cuda.synchronize()
+    check_linear(np_of(y), q, s, w, ws, bias, out)
+
+
+# R*ldx up to 2^31 is copied by the load unit, more is not; experts and rows of out lie further apart than 2^32 elements
+@pytest.mark.parametrize("sizes", [[2, 1, 3], [40, 0, 70], [300, 0, 290]])
+@pytest.mark.parametrize("ld", [1 << 20, 1 << 24])
+def test_grouped_of_rows_far_apart(sizes, ld):
+    c = Inputs(11, sizes, 150, 300, "fp8", True)
+    stride, sstride, ldo = (1 << 32) + 4, (1 << 30) + 1, max(1 << 23, ((1 << 32) // c.M) & ~1)
+    lds = (1 << 29) // c.R
+    xt, st = on(far(c.R, c.K, torch.uint8, ld), c.x), on(far(c.R, 3, torch.float32, lds), c.s)
+    wt, wst = far(c.E, c.N * c.K, torch.uint8, stride), far(c.E, 6, torch.float32, sstride)
+    on(wt, c.w.reshape(c.E, -1)), on(wst, c.ws.reshape(c.E, -1))
+    y = far(c.M, c.N, torch.bfloat16, ldo)
+    ot, rt = ints(c.offsets), ints(c.rows)
+    torch.cuda.synchronize()
+    abi.moe_grouped_linear(xt, abi.DT_FP8, ld, st, lds, c.R, rt, ot, c.E, c.M, wt, c.K, stride, wst, 3, sstride, c.N, c.K, y,
+                           abi.DT_BF16, ldo)
+    torch.cuda.synchronize()
+    c.check(np_of(y), "bf16")
+
+
+def test_rows_and_combine_far_apart():
+    T, K, ld = 5, 300, (1 << 30) + 1
+    x = oref.bf16(np.random.default_rng(12).standard_normal((T, K)))
+    xt, q, s = on(far(T, K, torch.bfloat16, ld), x), far(T, K, torch.uint8, ld), far(T, 3, torch.float32, ld)
+    torch.cuda.synchronize()
+    abi.moe_quant_fp8(xt, abi.DT_BF16, ld, abi.ACT_NONE, T, K, None, q, ld, s, ld)
+    torch.cuda.synchronize()
+    qw, sw = ref.quant(x)
+    assert np.array_equal(np_of(q), qw) and np.array_equal(np_of(s), sw)
+    del q, s
+    y = far(T, K, torch.bfloat16, ld)
+    torch.cuda.synchronize()
+    abi.moe_combine_rows(xt, abi.DT_BF16, ld, T, ints(np.arange(T)[::-1]), torch.full((T,), 2.0, device=DEV), xt, ld, T, 1, K, y,
+                         abi.DT_BF16, ld)
+    torch.cuda.synchronize()
+    want = oref.bf16((x + 2 * x[::-1]).astype(np.float32))          # exact in fp32 but for far exponents: one rounding
+    assert (np.abs(np_of(y) - want) <= 2.0 ** -8 * np.abs(want)).all()

@@ -19,6 +19,12 @@
 //         fp32, half the rate.  Taken for fp32 outputs, and where the weights'
 //         stream sets the time anyway.
 //   BF16  v_mfma_f32_16x16x32_bf16 on the values as they are, one running sum.
+// The unit's own rates here are 4130 TFLOP/s for F8 and 1900 for the others; widening
+// takes 7 cycles of a SIMD for two codes a lane.
+//
+// What sets the time: few rows, the stream of weights from HBM (6.35 TB/s by copies);
+// many rows, the matrix unit with the scaling of its results beside it; in between,
+// how many bytes are on their way per CU.  Weights are laid out as they come.
 #include "ops_common.h"
 
 namespace moe {
@@ -307,7 +313,7 @@ __device__ __forceinline__ void add_stage(v4f &acc, const Frag<MODE> &w, const F
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a stream of weights.  A block owns 16*RT weight rows and up to 8*TC
+// Few rows: a stream of weights, bound by HBM.  A block owns 16*RT weight rows and up to 8*TC
 // rows of x; its W waves take the stages in turn (a block reads W*128 neighbouring
 // bytes of each row) and their sums are added through LDS, in the waves' order.  A
 // wave works alone: it reads 8 rows x 128 bytes per load, neighbouring lanes on
@@ -317,6 +323,9 @@ __device__ __forceinline__ void add_stage(v4f &acc, const Frag<MODE> &w, const F
 // Scales: lane l loads those of token l%16 for the wave's stage l/16 of the next
 // four, and the weights' for its next 64 stages, and passes them on when their
 // stage comes.
+// Bytes on their way are what counts: a row of 6144 x 6144 7.0 us (5.4 TB/s) with 8 waves
+// of 16 rows, 24576 x 6144 23.1 (6.5); 16 tokens to 8 each of 256 experts of
+// 4096 x 6144 280 us.
 // ---------------------------------------------------------------------------
 template <int MODE, typename OT, bool GROUPED, bool NT, int RT, int TC, int W>
 __global__ __launch_bounds__(64 * W, 2) void product_stream_kernel(ProdArgs a, int tiles_n)
@@ -492,6 +501,26 @@ __global__ __launch_bounds__(64 * W, 2) void product_stream_kernel(ProdArgs a, i
 // Scales: the weights' of all stages lie in LDS from the beginning, the rows'
 // come four stages at a time (16 bytes of a row of scales; one by one they would
 // be a line each) into one of two places while the other is read.
+// A partial last stage comes by the same copies and is cleared in LDS past the rows'
+// end before it is read: 333 x 5003 x 2000 11.6 us, x 2048 11.3.
+//
+// Measured, in us, for bf16 outputs (F8; tiles of rows x channels):
+//                        64x64  64x128  128x128  128x256  256x256
+//     64 x  6144 x 6144   19.1    21.1     26.8     38.7     62.9   (streams: 11.6)
+//    333 x  5003 x 2048   10.9    10.1     12.2     17.2     27.8
+//    128 x 24576 x 6144   46.5    37.0     31.8     41.9     64.5
+//    600 x  8192 x 4096   45.2    37.1     39.0     30.7     46.7
+//   4096 x 24576 x 6144   1168     916      794      620      525
+// and for fp32 outputs (F8X):
+//     64 x  6144 x 6144   29.6    38.0     51.1     78.6            (streams: 14.7)
+//    333 x  5003 x 2048   16.5    16.9     21.1     31.6
+//    512 x  6144 x 6144   63.2    62.5     52.9     79.7
+//    600 x  8192 x 4096   66.2    63.2     70.0     56.8
+//   4096 x 12288 x 6144    773     654      612      506
+// 525 us are 2360 TFLOP/s, the unit 57 % busy at the 1.9 GHz that the card holds under
+// it: without the copies 17 % less, without the scaling 11 %, without the stores 7 %.
+// F8X's small tiles are bound by the widening, done by each wave for its own
+// fragments; widened once into LDS, the reads of twice the bytes would take as long.
 // ---------------------------------------------------------------------------
 constexpr int MAX_BLOCKS = 1024;                     // blocks of 128 codes in a row
 
@@ -845,7 +874,13 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void product_tiles_kernel(ProdArgs
 }
 
 // The rows of a group, up to 256 at a time, as a tile of as many as there are: 64, 128,
-// 192 or 256 x 256 channels.
+// 192 or 256 x 256 channels, so that weights are read once for up to 256 rows and few rows
+// cost few products.  Against tiles of one shape (64x128 / 128x256 / these, us):
+//   1024 tokens x 8 of 256 experts of 4096 x 6144   1185 / 1160 / 1135  (HBM, 5.6 TB/s)
+//   4096 x 8 of 256                                  1931 / 1605 / 1560
+//   4096 x 8 of  64 of 2048 x 2048                    273 /  199 /  176
+// 4096 x 8 of 256 is 1020 us of products and 1030 of weights, which two stages on their way
+// overlap in part: 1165 with all weights in L2.  A third stage has no room in LDS.
 template <int MODE, typename OT, bool DMA>
 __global__ __launch_bounds__(512, 2) void product_groups_kernel(ProdArgs a, int tiles_n)
 {
@@ -917,6 +952,8 @@ static bool copies_rows(const ProdArgs &a)
            a.ldw <= NEAR / 256 && a.ldx <= NEAR / (a.rows ? a.R : 256);
 }
 
+// A tile's time: of a stage, of the rest, and what is added to a stage where the last
+// round has a CU alone with one block.  Fitted to the times above and some 20 more.
 struct TileCost {
     int bt, bn;
     double stage, fixed, alone;                      // us
@@ -943,6 +980,8 @@ static int cheapest(const TileCost (&c)[N], const ProdArgs &a)
 template <int MODE, typename OT>
 static void enqueue_dense_tiles(const ProdArgs &a, hipStream_t st)
 {
+    // through registers: two shapes, by whether the larger fills the card (333 x 5003 x 2048: 64 x 64
+    // 18.1 us, 128 x 128 23.2; 1024 x 6144 x 6144 125 and 125; 4096 rows 459 and 370)
     if (!copies_rows(a)) {
         if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= CUS)
             launch_tiles<MODE, OT, false, false, 2, 4, 2, 2, 4>(a, st);
@@ -972,6 +1011,16 @@ static void enqueue_dense_tiles(const ProdArgs &a, hipStream_t st)
     }
 }
 
+// Streams as long as their blocks fit the card: a block has its K in W parts at once, where
+// a tile's stages come one after the other at 0.4 us each (64 x 6144 x 6144: stream 11.6 us,
+// tile 20.2; 256 x 2048 x 7168 12.4 and 23.2; 64 x 4096 x 7168 9.0 and 22.9; of fp32
+// 64 x 6144 x 6144 14.7 and 28.8).  With half as many blocks again it is the same
+// (128 x 6144 x 2048 9.3 and 9.0), with more the tiles win (256 x 6144 x 6144 28.3 and
+// 23.2).  Smaller blocks while they fit: of 16 channels, 32, then 64 (64 x 4096 x 7168:
+// 12.7, 9.0, 11.7; 48 x 2048 x 7168 of F8X: 7.9, 10.0), of 8 rows if there are no more; 16
+// waves where they alone fill the card (1 x 2048 x 7168 4.5 us, 8 waves 4.8; 1 x 6144 x 6144
+// 8.0 and 7.0).  Up to 32 rows all are streams (32 x 24576 x 6144 24.8, tiles 24.6; 32 x 8192 x
+// 7168 11.5 and 24.2).
 template <int MODE, int TILE_MODE, typename OT>
 static void enqueue_dense(const ProdArgs &a, hipStream_t st)
 {
@@ -986,21 +1035,59 @@ static void enqueue_dense(const ProdArgs &a, hipStream_t st)
             launch_stream<MODE, OT, false, false, 1, 2, 8>(a, st);
         else
             launch_stream<MODE, OT, false, false, 2, 2, 8>(a, st);
-    } else if (blocks(32, 16) <= CUS) {
-        launch_stream<MODE, OT, false, false, 1, 4, 8>(a, st);
-    } else if (blocks(32, 32) <= CUS) {
-        launch_stream<MODE, OT, false, false, 2, 4, 8>(a, st);
     } else if (a.M <= 32) {
-        launch_stream<MODE, OT, false, false, 2, 4, 4>(a, st);
+        if (blocks(32, 16) <= CUS)
+            launch_stream<MODE, OT, false, false, 1, 4, 8>(a, st);
+        else if (blocks(32, 32) <= CUS)
+            launch_stream<MODE, OT, false, false, 2, 4, 8>(a, st);
+        else
+            launch_stream<MODE, OT, false, false, 2, 4, 4>(a, st);
+    } else if (blocks(32, 16) <= CUS) {
+        launch_stream<TILE_MODE, OT, false, false, 1, 4, 8>(a, st);
+    } else if (blocks(32, 32) <= CUS) {
+        launch_stream<TILE_MODE, OT, false, false, 2, 4, 8>(a, st);
+    } else if (blocks(32, 64) <= CUS) {
+        launch_stream<TILE_MODE, OT, false, false, 4, 4, 4>(a, st);
     } else {
         enqueue_dense_tiles<TILE_MODE, OT>(a, st);
     }
 }
 
+// Few blocks in all, as a router's logits are: whatever the groups' sizes, K in eight parts.
+// 64 rows in 2 groups of 256 x 6144 of bf16 6.2 us (tiles 32, 16-row streams 8.9), 128 rows 6.9 in
+// blocks of 16 rows and 8.7 of 8, 1000 rows 14.5 (tiles 34); 100 x 4 of 8 of 512 x 4096
+// 7.8 (tiles 16.8).  False where there are more.
+template <int MODE, typename OT>
+static bool enqueue_few(const ProdArgs &a, int64_t rows, hipStream_t st)
+{
+    const auto blocks = [&](int t, int n) { return (a.E < a.M ? a.E : a.M) * ceil_div(rows, t) * ceil_div(a.N, n); };
+    if (blocks(8, 16) <= CUS / 2)
+        launch_stream<MODE, OT, true, false, 1, 1, 8>(a, st);
+    else if (blocks(16, 16) <= CUS)
+        launch_stream<MODE, OT, true, false, 1, 2, 8>(a, st);
+    else if (blocks(32, 32) <= CUS)
+        launch_stream<MODE, OT, true, false, 2, 4, 8>(a, st);
+    else
+        return false;
+    return true;
+}
+
+// By the rows of a group on average.  Streams up to 12 (24 where tiles have the bf16 unit too):
+// E4M3, 64 experts of 2048 x 2048 with 16 rows each 44.9 us and tiles 41.5, of bf16 105.8 and
+// 114.5, 24 rows 115 and 123, 32 rows 117.6 and 117.0.  Weights that pass the caches are read
+// so too: 256 of 4096 x 6144 by 16 tokens x 8 280 us and 317, by 256 tokens 897 and 938;
+// where they stay in them not: 64 of 2048 x 2048 by 64 tokens 48 and 40.
+// Tiles: 64 x 128 below 24 rows (bf16 64: 125 rows 157 us, groups' tiles 151, 32 rows
+// 116 and 146) and where the groups' do not fill the card (16 experts of 2048 x 4096, 64 rows each
+// 28 us, groups' 47; 512 rows each 125 and 107).  F8X: 64 x 128 below 128 rows (125
+// rows 123 us, 128 x 256 136; 512 rows 402 and 312).  Rows that are not copied: 64 x 64 below
+// 128 (125 rows 197 us, 128 x 128 205; 256 rows 328 and 295).
 template <int MODE, int TILE_MODE, typename OT>
 static void enqueue_grouped(const ProdArgs &a, hipStream_t st)
 {
-    const int64_t rows = ceil_div(a.M, a.E);         // of a group on average
+    const int64_t rows = ceil_div(a.M, a.E);
+    if (rows <= 12 ? enqueue_few<MODE, OT>(a, rows, st) : enqueue_few<TILE_MODE, OT>(a, rows, st))
+        return;
     // weights that the last-level cache does not keep from one call to the next, and
     // that hardly anyone reads twice
     const bool passing = (int64_t)(a.E < a.M ? a.E : a.M) * a.N * a.K >= (512ll << 20);
@@ -1009,8 +1096,8 @@ static void enqueue_grouped(const ProdArgs &a, hipStream_t st)
             launch_stream<MODE, OT, true, true, 2, 2, 4>(a, st);
         else
             launch_stream<MODE, OT, true, false, 2, 2, 4>(a, st);
-    } else if (rows <= 12) {
-        if (passing)
+    } else if (rows <= (TILE_MODE == F8 ? 12 : 24)) {
+        if (passing && rows <= 12)
             launch_stream<MODE, OT, true, true, 4, 4, 4>(a, st);
         else
             launch_stream<MODE, OT, true, false, 4, 4, 4>(a, st);

@@ -197,6 +197,16 @@ def test_linear_tiles(out, T, N, K, pad, shift):
     check_linear(run_linear(q, s, w, ws, bias, out, pad, shift, pad), q, s, w, ws, bias, out)
 
 
+# Some rows, of so many channels that the blocks of a stream are 16, 32 and 64 channels wide, and a
+# few more, where they are tiles.
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N", [(33, 2040), (40, 4050), (64, 4100), (33, 8190), (200, 2250), (64, 9000), (300, 60), (2100, 7)])
+@pytest.mark.parametrize("K,pad,shift", [(520, 8, 8), (1300, 4, 4), (700, 3, 1), (7, 0, 0)])
+def test_linear_between_streams_and_tiles(out, T, N, K, pad, shift):
+    q, s, w, ws, bias = linear_inputs(14, T, N, K)
+    check_linear(run_linear(q, s, w, ws, bias, out, pad, shift, pad), q, s, w, ws, bias, out)
+
+
 # rows on 4 bytes whose length is not of whole words: the last row's last word is partly behind it
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("T,N", [(40, 300), (320, 5003), (512, 5000), (1100, 4600), (2100, 4700)])

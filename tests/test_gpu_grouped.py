@@ -156,6 +156,24 @@ def test_grouped_tiles(xd, out, K, pad, shift, mean):
     c.check(c.run(out, pad, shift, pad), out)
 
 
+# few blocks in all, in blocks of 8, 16 and 32 rows; the last of more rows to an expert
+@pytest.mark.parametrize("xd", ["fp8", "bf16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("sizes", [[1], [7], [60], [129], [500], [3, 0, 0], [90, 0, 1, 40], [2, 3, 1, 0, 1, 2, 4, 3], [0, 1000]])
+@pytest.mark.parametrize("N,K", [(250, 1300), (62, 77)])
+def test_grouped_few_blocks(xd, out, sizes, N, K):
+    c = Inputs(12, sizes, N, K, xd, len(sizes) > 1)
+    c.check(c.run(out, 4, 4, 4), out)
+
+
+# groups of 13 to 24 rows on average
+@pytest.mark.parametrize("xd", ["fp8", "bf16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_grouped_of_some_rows(xd, out):
+    c = Inputs(13, [20, 0, 33, 1, 64, 16, 5, 8] * 4, 1100, 600, xd, True)
+    c.check(c.run(out), out)
+
+
 # rows on 4 bytes whose length is not of whole words: the last row's last word is partly behind it
 @pytest.mark.parametrize("xd", ["fp8", "bf16"])
 @pytest.mark.parametrize("out", ["bf16", "f32"])

@@ -665,10 +665,11 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     // channels.  x and its scales are read LA steps ahead, w in the stage's last step,
     // each in the place of the fragment that was just used; products are scaled and
     // added LAG products later.  Before step TURN, whose x is the next stage's, nothing
-    // of this stage is left to be read but w: the waves meet, and stage st + NB sets
+    // of this stage is left to be read but w: the waves meet, and stage st + AHEAD sets
     // out over it, a copy at a time between the products (all at once they fill the
     // load unit's queue, and what is behind them waits).
     constexpr int XR = FT % 4 == 0 ? 4 : FT % 3 == 0 ? 3 : 2, LA = XR - 1, TURN = FT - LA, LAG = 2, SLOTS = LA * FN;
+    constexpr int AHEAD = DMA ? NB : 2;              // registers hold one stage
     static_assert(FT % XR == 0 && FT % 2 == 0 && FN % LAG == 0, "places change the same way in each stage");
     Frag<MODE> wf[FN], xf[XR];
     v4f p[LAG];                                      // products not yet added
@@ -752,7 +753,7 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
                 if constexpr (i >= TURN) {
 #pragma unroll
                     for (int c = slot * CP / SLOTS; c < (slot + 1) * CP / SLOTS; ++c)
-                        fetch(c, cur, st + NB);
+                        fetch(c, cur, st + AHEAD);
                     if constexpr (i == FT - 1)
                         read_w(wf[j], next, j);
                 }
@@ -773,9 +774,8 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     };
     bring(0);
     bring(1);
-    // registers hold one stage, so that there is one less on its way
 #pragma unroll
-    for (int b = 0; b < (DMA ? NB : 2); ++b) {
+    for (int b = 0; b < AHEAD; ++b) {
 #pragma unroll
         for (int i = 0; i < CP; ++i)
             fetch(i, b * BUF, b);
@@ -980,13 +980,24 @@ static int cheapest(const TileCost (&c)[N], const ProdArgs &a)
 template <int MODE, typename OT>
 static void enqueue_dense_tiles(const ProdArgs &a, hipStream_t st)
 {
-    // through registers: two shapes, by whether the larger fills the card (333 x 5003 x 2048: 64 x 64
-    // 18.1 us, 128 x 128 23.2; 1024 x 6144 x 6144 125 and 125; 4096 rows 459 and 370)
+    // Through registers, a piece crossing words and lines: 333 x 5003 x 2048 with 64x64 / 64x128 / 128x256
+    // 18.0 / 19.0 / 31.1 us, 512 x 6144 x 6144 69.7 / 62.8 / 89, 4096 x 6144 x 6144 493 / 353 / 266 (copied
+    // 140); fp32 outputs 23 / 23 / 46, 80 / 135 / 138 and 567 / 796 / 414.  256x256 has too few registers (477).
     if (!copies_rows(a)) {
-        if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= CUS)
-            launch_tiles<MODE, OT, false, false, 2, 4, 2, 2, 4>(a, st);
-        else
-            launch_tiles<MODE, OT, false, false, 2, 2, 2, 2, 2>(a, st);
+        if constexpr (MODE == F8) {
+            static constexpr TileCost cost[] = {{64, 64, 0.40, 1.5, 0.25}, {64, 128, 0.60, 2.0, 0.3}, {128, 256, 1.8, 4.0, 0.0}};
+            switch (cheapest(cost, a)) {
+            case 0: launch_tiles<MODE, OT, false, false, 2, 2, 2, 2, 2>(a, st); break;
+            case 1: launch_tiles<MODE, OT, false, false, 2, 2, 4, 2, 2>(a, st); break;
+            default: launch_tiles<MODE, OT, false, false, 2, 2, 4, 4, 4>(a, st); break;
+            }
+        } else {
+            static constexpr TileCost cost[] = {{64, 64, 0.46, 1.5, 0.2}, {128, 256, 2.8, 4.0, 0.0}};
+            if (cheapest(cost, a) == 0)
+                launch_tiles<MODE, OT, false, false, 2, 2, 2, 2, 2>(a, st);
+            else
+                launch_tiles<MODE, OT, false, false, 2, 2, 4, 4, 4>(a, st);
+        }
         return;
     }
     if constexpr (MODE == F8) {
@@ -1015,8 +1026,10 @@ static void enqueue_dense_tiles(const ProdArgs &a, hipStream_t st)
 // a tile's stages come one after the other at 0.4 us each (64 x 6144 x 6144: stream 11.6 us,
 // tile 20.2; 256 x 2048 x 7168 12.4 and 23.2; 64 x 4096 x 7168 9.0 and 22.9; of fp32
 // 64 x 6144 x 6144 14.7 and 28.8).  With half as many blocks again it is the same
-// (128 x 6144 x 2048 9.3 and 9.0), with more the tiles win (256 x 6144 x 6144 28.3 and
-// 23.2).  Smaller blocks while they fit: of 16 channels, 32, then 64 (64 x 4096 x 7168:
+// (128 x 6144 x 2048 9.3 and 9.0; of fp32 128 x 6144 x 6144 23.3 and 30.4), with more the tiles win
+// (256 x 6144 x 6144 28.3 and 23.2).  Where rows are not copied the tiles take twice as long, the
+// streams half as much again (128 x 6144 x 6144 34.6 and 45.5, 256 rows 50.2 and 47.2; of fp32 256
+// rows 53.4 and 68.5), so they go on to 2 or 3 blocks for each CU.  Smaller blocks while they fit: of 16 channels, 32, then 64 (64 x 4096 x 7168:
 // 12.7, 9.0, 11.7; 48 x 2048 x 7168 of F8X: 7.9, 10.0), of 8 rows if there are no more; 16
 // waves where they alone fill the card (1 x 2048 x 7168 4.5 us, 8 waves 4.8; 1 x 6144 x 6144
 // 8.0 and 7.0).  Up to 32 rows all are streams (32 x 24576 x 6144 24.8, tiles 24.6; 32 x 8192 x
@@ -1046,7 +1059,7 @@ static void enqueue_dense(const ProdArgs &a, hipStream_t st)
         launch_stream<TILE_MODE, OT, false, false, 1, 4, 8>(a, st);
     } else if (blocks(32, 32) <= CUS) {
         launch_stream<TILE_MODE, OT, false, false, 2, 4, 8>(a, st);
-    } else if (blocks(32, 64) <= CUS) {
+    } else if (2 * blocks(32, 64) <= CUS * (copies_rows(a) ? (TILE_MODE == F8 ? 2 : 3) : (TILE_MODE == F8 ? 4 : 6))) {
         launch_stream<TILE_MODE, OT, false, false, 4, 4, 4>(a, st);
     } else {
         enqueue_dense_tiles<TILE_MODE, OT>(a, st);
@@ -1080,8 +1093,10 @@ static bool enqueue_few(const ProdArgs &a, int64_t rows, hipStream_t st)
 // Tiles: 64 x 128 below 24 rows (bf16 64: 125 rows 157 us, groups' tiles 151, 32 rows
 // 116 and 146) and where the groups' do not fill the card (16 experts of 2048 x 4096, 64 rows each
 // 28 us, groups' 47; 512 rows each 125 and 107).  F8X: 64 x 128 below 128 rows (125
-// rows 123 us, 128 x 256 136; 512 rows 402 and 312).  Rows that are not copied: 64 x 64 below
-// 128 (125 rows 197 us, 128 x 128 205; 256 rows 328 and 295).
+// rows 123 us, 128 x 256 136; 512 rows 402 and 312).  Rows that are not copied (64 experts of
+// 2048 x 2048): E4M3 64 x 128 below 256 rows (125 rows 160 us, 128 x 256 170; 512 rows 481 and 373); on
+// the bf16 unit streams up to 64 (32 rows 97, 128 x 256 123; 64 rows 167 and 181; of bf16 236 and the
+// groups' tiles 277), then F8X 128 x 256, bf16 the groups' tiles (125 rows 290, 128 x 256 338).
 template <int MODE, int TILE_MODE, typename OT>
 static void enqueue_grouped(const ProdArgs &a, hipStream_t st)
 {
@@ -1096,16 +1111,18 @@ static void enqueue_grouped(const ProdArgs &a, hipStream_t st)
             launch_stream<MODE, OT, true, true, 2, 2, 4>(a, st);
         else
             launch_stream<MODE, OT, true, false, 2, 2, 4>(a, st);
-    } else if (rows <= (TILE_MODE == F8 ? 12 : 24)) {
+    } else if (rows <= (TILE_MODE == F8 ? 12 : copies_rows(a) ? 24 : 64)) {
         if (passing && rows <= 12)
             launch_stream<MODE, OT, true, true, 4, 4, 4>(a, st);
         else
             launch_stream<MODE, OT, true, false, 4, 4, 4>(a, st);
     } else if (!copies_rows(a)) {
-        if (rows >= 128)
-            launch_tiles<TILE_MODE, OT, true, false, 2, 4, 2, 2, 4>(a, st);
+        if constexpr (TILE_MODE == BF16)
+            launch_groups<BF16, OT, false>(a, st);
+        else if (TILE_MODE == F8 && rows < 256)
+            launch_tiles<TILE_MODE, OT, true, false, 2, 2, 4, 2, 2>(a, st);
         else
-            launch_tiles<TILE_MODE, OT, true, false, 2, 2, 2, 2, 2>(a, st);
+            launch_tiles<TILE_MODE, OT, true, false, 2, 2, 4, 4, 4>(a, st);
     } else if constexpr (TILE_MODE == F8X) {
         if (rows < 128)
             launch_tiles<F8X, OT, true, true, 3, 2, 4, 2, 2>(a, st);

@@ -174,6 +174,15 @@ def test_grouped_of_some_rows(xd, out):
     c.check(c.run(out), out)
 
 
+# many rows to an expert, on 16 bytes and on single ones
+@pytest.mark.parametrize("xd", ["fp8", "bf16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("K,pad,shift", [(256, 0, 0), (300, 3, 1)])
+def test_grouped_of_many_rows(xd, out, K, pad, shift):
+    c = Inputs(14, [400, 0, 257, 900], 2600, K, xd, True)
+    c.check(c.run(out, pad, shift, pad), out)
+
+
 # rows on 4 bytes whose length is not of whole words: the last row's last word is partly behind it
 @pytest.mark.parametrize("xd", ["fp8", "bf16"])
 @pytest.mark.parametrize("out", ["bf16", "f32"])

@@ -339,7 +339,7 @@ moe_status moe_router_topk_grouped(moe_ctx *ctx, const moe_route_desc *desc, con
  *
  * moe_linear_fp8: out[t,n] = bias[n] + sum_b (sum_{k in b} q[t,k]*w[n,k]) *
  * (s[t,b]*ws[n/128,b]); the sums over blocks in fp32, bias [N] or NULL.  Those of a block
- * are fp32 too where out is MOE_DT_F32, and where rows are few (T up to 32 at least; up to
+ * are fp32 too where out is MOE_DT_F32, and where rows are few (T up to 32; up to
  * 12 in a group on average); else, for MOE_DT_BF16, they are the E4M3 matrix unit's: it
  * aligns 8 neighbouring products to the largest and drops what lies 2^-13 of that
  * one's power of two below (1.4e-5 of a sum of normal codes; a rounding to bf16 is

@@ -25,6 +25,7 @@
 // What sets the time: few rows, the stream of weights from HBM (6.4 to 7.0 TB/s);
 // many rows, the matrix unit with the scaling of its results beside it; in between,
 // how many bytes are on their way per CU.  Weights are laid out as they come.
+#include "copy_window.h"
 #include "ops_common.h"
 
 namespace moe {
@@ -212,8 +213,8 @@ __device__ __forceinline__ const uint8_t *uniform(const void *p)
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
     return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
 }
-// `bytes` of memory at p as the load unit's buffer: what lies outside reads as 0, and
-// is not read
+// `bytes` of memory at p as the load unit's buffer: a word at an offset that is not all
+// inside reads as 0
 __device__ __forceinline__ v4i buffer_of(const uint8_t *p, uint32_t bytes)
 {
     const uint64_t u = reinterpret_cast<uint64_t>(p);
@@ -221,17 +222,18 @@ __device__ __forceinline__ v4i buffer_of(const uint8_t *p, uint32_t bytes)
                __builtin_amdgcn_readfirstlane((int)((uint32_t)(u >> 32) & 0xffff)),
                __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
-// 16 bytes of each lane, at lane_at + at of a buffer, to LDS address `to` + 16 * lane.
+// 16 bytes of each lane, at lane_at of a buffer, to LDS address `to` + 16 * lane.  The
+// scalar offset is 0: what the unit checks is the lane's offset against the size.
 // In assembly: told of copies into LDS, the compiler waits for those on their way
 // before it reads LDS elsewhere, unless it can tell the places apart; here the
 // callers wait.  (m0 is the compiler's, and kept.)
-__device__ __forceinline__ void copy16(v4i from, uint32_t lane_at, int at, int to)
+__device__ __forceinline__ void copy16(v4i from, uint32_t lane_at, int to)
 {
     int m0;
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-                 "buffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+                 "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0)
-                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(lane_at), "s"(from), "s"(__builtin_amdgcn_readfirstlane(at))
+                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(lane_at), "s"(from)
                  : "memory");
 }
 // the same of 4 bytes, from an address of each lane
@@ -592,9 +594,10 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     }
     v4i reg[DMA ? 1 : CP];
     auto fetch = [&](int i, int buf, int st) INLINE {    // sets out copy i of stage st
-        if constexpr (DMA)
-            copy16(buffer_of(i < TP ? x0 : w0, st < stages ? (i < TP ? x_end : w_end) : 0u), lane_at[i], 128 * st,
-                   lds0 + buf + lds_at(i));
+        if constexpr (DMA) {                         // past the last stage from 0 bytes: zeros, nothing is read
+            const uint32_t at = 128 * (uint32_t)st, end = i < TP ? x_end : w_end;
+            copy16(buffer_of((i < TP ? x0 : w0) + at, st < stages ? window_bytes(end, at) : 0u), lane_at[i], lds0 + buf + lds_at(i));
+        }
         else if ((a.K & 127) && st >= stages - 1)
             reg[i] = load_piece_end(src[i] - 16 * piece, 128 * (stages - 1) + 16 * piece, a.K);
         else
@@ -621,14 +624,14 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     };
 
     // scales: a quad is those of four stages, in LDS as [row][4]
-    v4i s_rows = {0, 0, 0, 0};
-    uint32_t s_lane = 0;
+    const uint8_t *s_first = nullptr;
+    uint32_t s_end = 0, s_lane = 0;
     if constexpr (SCALED) {
-        const float *s0 = gathered ? a.s : a.s + (int64_t)t.row0 * a.lds;
+        s_first = uniform(gathered ? a.s : a.s + (int64_t)t.row0 * a.lds);
         const int r = min(64 * wave + lane, t.rows - 1);
         s_lane = (uint32_t)((gathered ? source_row<GROUPED>(a, t.row0 + r) : r) * a.lds * 4);
-        // its end is the last row's: what a quad has past it reads as 0
-        s_rows = buffer_of(uniform(s0), (uint32_t)(((int64_t)((gathered ? a.R : t.rows) - 1) * a.lds + stages) * 4));
+        // the last row's end: what a quad has past it reads as 0
+        s_end = (uint32_t)(((int64_t)((gathered ? a.R : t.rows) - 1) * a.lds + stages) * 4);
         for (int i = wave; i < S::WB * ((stages + 63) >> 6); i += NW) {
             const int b = i % S::WB, k = i / S::WB * 64;
             const float *row = t.ws + (int64_t)(min(t.n0 + 128 * b, a.N - 1) >> 7) * a.ldws;
@@ -637,7 +640,8 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     }
     auto bring = [&](int q) INLINE {                 // sets out a quad's copy
         if (SCALED && 64 * wave < BT && 4 * q < stages)
-            copy16(s_rows, s_lane, 16 * q, lds0 + S::TSCALE + 16 * (SROWS * (q & 1) + 64 * wave));
+            copy16(buffer_of(s_first + 16 * q, window_bytes(s_end, 16 * (uint32_t)q)), s_lane,
+                   lds0 + S::TSCALE + 16 * (SROWS * (q & 1) + 64 * wave));
     };
 
     v4f acc[FT][FN];

@@ -1,0 +1,60 @@
+"""CPU tests of what the products' copies into LDS may read: the size and the beginning of a copy's buffer
+leave nothing outside the rows within reach, whatever the load unit's check makes of a scalar offset."""
+import ctypes as C
+import glob
+import os
+import re
+import subprocess
+
+import pytest
+
+from quantized_expert_ffn_topk_amd import abi, build
+
+CSRC = os.path.join(abi.PKG, "csrc")
+
+
+def test_copies_have_no_scalar_offset():
+    """buffer_load .. lds in assembly: address register, descriptor, then the scalar offset, a literal 0."""
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(CSRC, "*"))):
+        for operands in re.findall(r"buffer_load_dword\w*\s+([^\"\\]*\blds\b)", open(path).read()):
+            seen += 1
+            assert re.fullmatch(r"%\d+, %\d+, 0 offen lds", operands), (os.path.basename(path), operands)
+    assert seen == 1
+
+
+@pytest.fixture(scope="module")
+def window(tmp_path_factory):
+    d = tmp_path_factory.mktemp("window")
+    source, lib = d / "w.cpp", d / "w.so"
+    source.write_text('#include "copy_window.h"\nextern "C" uint32_t window(uint32_t end, uint32_t at)\n'
+                      "{\n    return moe::window_bytes(end, at);\n}\n")
+    subprocess.run(build.CXX.split() + ["-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + CSRC, str(source), "-o", str(lib)],
+                   check=True)
+    f = C.CDLL(str(lib)).window
+    f.argtypes, f.restype = [C.c_uint32] * 2, C.c_uint32
+    return f
+
+
+# rows, their distance and length in bytes
+@pytest.mark.parametrize("rows,ld,K", [(1, 4, 1), (1, 128, 128), (3, 132, 129), (5, 300, 300), (64, 516, 513), (2, 1 << 20, 700),
+                                       (256, 1 << 23, 1 << 18)])
+def test_a_word_is_read_where_it_is_inside_and_nowhere_else(window, rows, ld, K):
+    """Stage st of a row's piece at lane offset r*ld + 16*c, word by word: read if all of it lies in the buffer."""
+    end = ((rows - 1) * ld + K + 3) & ~3
+    assert end < 1 << 32
+    for st in sorted({0, 1, (K - 1) // 128, (K - 1) // 128 + 1, end // 128, end // 128 + 1}):
+        at = 128 * st
+        size = window(end, at)
+        assert at + size <= max(end, at) and size == max(0, end - at)
+        for r in {0, rows // 2, rows - 1}:
+            for w in range(32):
+                off = r * ld + 4 * w
+                read = off + 4 <= size
+                assert read == (at + off + 4 <= end)             # no word behind the last row's
+                assert read or at + 4 * w >= K                   # and none of a row's own is missing
+
+
+def test_nothing_is_read_where_nothing_is_left(window):
+    for end, at in ((0, 0), (4, 4), (4, 128), (128, 256), (0, (1 << 32) - 1), ((1 << 31) + 4, 1 << 31), (1 << 31, (1 << 31) + 4)):
+        assert window(end, at) == max(0, end - at)

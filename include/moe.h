@@ -364,7 +364,7 @@ moe_status moe_router_topk_grouped(moe_ctx *ctx, const moe_route_desc *desc, con
  *
  * moe_combine_rows: out[t] = base[t] + sum_i gate_w[t,i] * y[pos[t,i]] in fp32, in the
  * order of i, for y [R,H], pos and gate_w [T,k]; base [T,H] of out's dtype, NULL for
- * zeros, and may be out itself (same ld).  A pos outside [0,R) adds nothing. */
+ * zeros, and may be out itself (then with the same ld).  A pos outside [0,R) adds nothing. */
 #define MOE_ACT_NONE   0
 #define MOE_ACT_SWIGLU 1
 moe_status moe_quant_fp8(const void *x, int32_t x_dtype, int64_t ldx, int32_t act, int32_t T,

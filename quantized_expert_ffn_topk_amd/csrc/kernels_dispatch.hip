@@ -352,6 +352,8 @@ extern "C" moe_status moe_combine_rows(const void *y, int32_t y_dtype, int64_t l
         return fail(MOE_E_INVAL, "y/pos/gate_w/out is NULL");
     if ((R > 0 && ldy < H) || (base && ldb < H) || ldo < H)
         return fail(MOE_E_INVAL, "a leading dimension is below H=%d", H);
+    if (base == out && T > 1 && ldb != ldo)          // a row of out would be another one's base
+        return fail(MOE_E_INVAL, "base is out, but ldb=%lld and ldo=%lld", (long long)ldb, (long long)ldo);
     const size_t os = out_dtype == MOE_DT_F32 ? 4 : 2;
     if (!ops_aligned(y, y_dtype == MOE_DT_F32 ? 4 : 2) || !ops_aligned(pos, 4) || !ops_aligned(gate_w, 4) ||
         !ops_aligned(base, os) || !ops_aligned(out, os))

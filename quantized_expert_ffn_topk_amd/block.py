@@ -78,11 +78,13 @@ def quantise_weight_fp8(w):
     amax = by.abs().amax(dim=(-1, -3))
     fine = torch.isfinite(amax)
     pre = torch.ones_like(amax).masked_fill(amax < 2.0 ** -96, 2.0 ** 64)
-    inv = torch.where(fine & (amax > 0), 448.0 / (amax * pre), 0.0)
+    # quotients of tensors, each rounded once: with a number, torch's are a reciprocal and a product
+    top = torch.full_like(amax, 448.0)
+    inv = torch.where(fine & (amax > 0), top / (amax * pre), 0.0)
     at = lambda v: v[..., :, None, :, None]  # noqa: E731
     q = torch.where(at(fine), (by * at(pre)) * at(inv), 0.0).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
     q = q.flatten(-4, -3).flatten(-2, -1)[..., :N, :K]
-    return q.contiguous(), torch.where(fine, amax / 448.0, float("nan"))
+    return q.contiguous(), torch.where(fine, amax / top, float("nan"))
 
 
 def _blocks(n):

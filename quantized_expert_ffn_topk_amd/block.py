@@ -256,50 +256,59 @@ class MoEFFN(_Norm):
         return out, h
 
 
-class Fp8DenseFFN(_Norm):
+class _Fp8FFN:
+    """A SwiGLU FFN of E4M3 weights between codes and rows: gate_up [2F, H] with s_gu,
+    down [H, F] with s_dn, and the rows between its products for up to max_tokens rows."""
+
+    def __init__(self, H, dev, gate_up, s_gu, down, s_dn, max_tokens):
+        import torch as t
+        if gate_up.dim() != 2 or down.dim() != 2:
+            raise ValueError("gate_up and down must be matrices")
+        self.H, F = H, down.shape[1]
+        self.F = F
+        self.gate_up, self.s_gu = _fp8_weights(t, gate_up, s_gu, (2 * F, H), "gate_up")
+        self.down, self.s_dn = _fp8_weights(t, down, s_dn, (H, F), "down")
+        if any(a.device != dev for a in (self.gate_up, self.down, self.s_gu, self.s_dn)):
+            raise ValueError("weights and gamma must be on one device")
+        e = lambda *shape, dt: t.empty((max_tokens,) + shape, dtype=dt, device=dev)  # noqa: E731
+        self.gu = e(2 * F, dt=t.bfloat16)
+        self.qh, self.sh = e(F, dt=t.float8_e4m3fn), e(_blocks(F), dt=t.float32)
+
+    def products(self, T, q, s, out, stream):
+        """out [T, H] from codes q [T, H] with scales s."""
+        H, F, hb, fb = self.H, self.F, _blocks(self.H), _blocks(self.F)
+        abi.moe_linear_fp8(q, H, s, hb, T, self.gate_up, H, self.s_gu, hb, None, 2 * F, H, self.gu, abi.DT_BF16, 2 * F, stream)
+        abi.moe_quant_fp8(self.gu, abi.DT_BF16, 2 * F, abi.ACT_SWIGLU, T, F, None, self.qh, F, self.sh, fb, stream)
+        abi.moe_linear_fp8(self.qh, F, self.sh, fb, T, self.down, F, self.s_dn, fb, None, H, F, out, _dtype(out), H, stream)
+
+
+class Fp8DenseFFN(_Norm, _Fp8FFN):
     """A dense SwiGLU FFN with E4M3 weights: gate_up [2F, H] (the gate rows above the
     up rows) with scales s_gu [ceil(2F/128), ceil(H/128)], down [H, F] with s_dn
     [ceil(H/128), ceil(F/128)] (quantise_weight_fp8 makes them)."""
 
     def __init__(self, gamma, gate_up, s_gu, down, s_dn, max_tokens, eps=1e-6, out_dtype=None):
-        super().__init__(gamma, max_tokens, eps)
-        t, H = self.torch, self.H
-        if gate_up.dim() != 2 or down.dim() != 2:
-            raise ValueError("gate_up and down must be matrices")
-        F = self.F = down.shape[1]
-        self.gate_up, self.s_gu = _fp8_weights(t, gate_up, s_gu, (2 * F, H), "gate_up")
-        self.down, self.s_dn = _fp8_weights(t, down, s_dn, (H, F), "down")
-        if any(a.device != self.dev for a in (self.gate_up, self.down, self.s_gu, self.s_dn)):
-            raise ValueError("weights and gamma must be on one device")
+        _Norm.__init__(self, gamma, max_tokens, eps)
+        t, H, n = self.torch, self.H, self.max_tokens
+        _Fp8FFN.__init__(self, H, self.dev, gate_up, s_gu, down, s_dn, n)
         self.out_dtype = out_dtype or t.bfloat16
         if self.out_dtype not in (t.float32, t.bfloat16):
             raise ValueError("out_dtype must be fp32 or bf16, not %s" % self.out_dtype)
-        n = self.max_tokens
         e = lambda *shape, dt: t.empty(shape, dtype=dt, device=self.dev)  # noqa: E731
-        self.y, self.gu = e(n, H, dt=t.bfloat16), e(n, 2 * F, dt=t.bfloat16)
+        self.y = e(n, H, dt=t.bfloat16)
         self.q, self.s = e(n, H, dt=t.float8_e4m3fn), e(n, _blocks(H), dt=t.float32)
-        self.qh, self.sh = e(n, F, dt=t.float8_e4m3fn), e(n, _blocks(F), dt=t.float32)
         self._made()
 
     def forward(self, x, residual, stream=None):
         """As DenseFFN.forward."""
-        H, F = self.H, self.F
+        H = self.H
         rows = self._check(x, residual)
         with self._on(stream, x, residual):
             T, h = self._norm(x, residual, rows, self.y, None, None, stream)
             out = self.torch.empty((T, H), dtype=self.out_dtype, device=self.dev)
             abi.moe_quant_fp8(self.y, abi.DT_BF16, H, abi.ACT_NONE, T, H, None, self.q, H, self.s, _blocks(H), stream)
-            _fp8_ffn(self, T, self.q, self.s, out, stream)
+            self.products(T, self.q, self.s, out, stream)
         return out, h
-
-
-def _fp8_ffn(w, T, q, s, out, stream):
-    """The two products of an E4M3 FFN and what is between, for codes q [T, H] with scales s."""
-    H, F = w.H, w.F
-    abi.moe_linear_fp8(q, H, s, _blocks(H), T, w.gate_up, H, w.s_gu, _blocks(H), None, 2 * F, H, w.gu, abi.DT_BF16, 2 * F,
-                       stream)
-    abi.moe_quant_fp8(w.gu, abi.DT_BF16, 2 * F, abi.ACT_SWIGLU, T, F, None, w.qh, F, w.sh, _blocks(F), stream)
-    abi.moe_linear_fp8(w.qh, F, w.sh, _blocks(F), T, w.down, F, w.s_dn, _blocks(F), None, H, F, out, _dtype(out), H, stream)
 
 
 class Fp8MoEFFN(_Norm):
@@ -334,7 +343,7 @@ class Fp8MoEFFN(_Norm):
         self.route = route
         self.shared = None
         if shared is not None:
-            self.shared = Fp8DenseFFN(self.gamma, *shared, max_tokens=max_tokens, eps=eps, out_dtype=self.out_dtype)
+            self.shared = _Fp8FFN(H, self.dev, *shared, max_tokens=self.max_tokens)
         n, m = self.max_tokens, self.max_tokens * k
         e = lambda *shape, dt: t.empty(shape, dtype=dt, device=self.dev)  # noqa: E731
         self.y, self.logits = e(n, H, dt=t.bfloat16), e(n, E, dt=t.float32)
@@ -347,7 +356,7 @@ class Fp8MoEFFN(_Norm):
         self.qh, self.sh = e(m, F, dt=t.float8_e4m3fn), e(m, _blocks(F), dt=t.float32)
         self._made()
         if self.shared is not None:
-            self._own += self.shared._own
+            self._own += [a for a in vars(self.shared).values() if isinstance(a, t.Tensor)]
 
     def forward(self, x, residual, stream=None):
         """As DenseFFN.forward; the chosen experts and their weights are in idx[:T] and
@@ -370,7 +379,7 @@ class Fp8MoEFFN(_Norm):
             abi.moe_grouped_linear(self.qh, abi.DT_FP8, F, self.sh, fb, M, None, self.offsets, E, M, self.down, F, H * F,
                                    self.s_dn, fb, hb * fb, H, F, self.yr, abi.DT_BF16, H, stream)
             if self.shared is not None:
-                _fp8_ffn(self.shared, T, self.q, self.s, out, stream)
+                self.shared.products(T, self.q, self.s, out, stream)
             abi.moe_combine_rows(self.yr, abi.DT_BF16, H, M, self.pos, self.w, out if self.shared is not None else None, H, T, k, H,
                                  out, _dtype(out), H, stream)
         return out, h

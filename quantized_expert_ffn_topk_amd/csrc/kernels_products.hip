@@ -27,6 +27,7 @@
 // how many bytes are on their way per CU.  Weights are laid out as they come.
 #include "copy_window.h"
 #include "ops_common.h"
+#include "products_choice.h"
 
 namespace moe {
 
@@ -35,8 +36,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
-enum { F8 = 0, F8X = 1, BF16 = 2 };
 
 struct ProdArgs {
     const uint8_t *x, *w;
@@ -245,7 +244,6 @@ __device__ __forceinline__ void copy4(const void *from, int to)
                  : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
                  : "memory");
 }
-constexpr int64_t NEAR = 1ll << 31;                  // bytes from a buffer's beginning that lane offsets reach
 
 // ---------------------------------------------------------------------------
 // A row's part of a stage in a lane: two pieces (32 bytes) of row l%16, the same
@@ -597,11 +595,11 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
         if constexpr (DMA) {                         // past the last stage from 0 bytes: zeros, nothing is read
             const uint32_t at = 128 * (uint32_t)st, end = i < TP ? x_end : w_end;
             copy16(buffer_of((i < TP ? x0 : w0) + at, st < stages ? window_bytes(end, at) : 0u), lane_at[i], lds0 + buf + lds_at(i));
-        }
-        else if ((a.K & 127) && st >= stages - 1)
+        } else if ((a.K & 127) && st >= stages - 1) {
             reg[i] = load_piece_end(src[i] - 16 * piece, 128 * (stages - 1) + 16 * piece, a.K);
-        else
+        } else {
             reg[i] = load_piece(src[i] + 128 * min(st, stages - 1));
+        }
     };
     auto land = [&](int buf) INLINE {
         if constexpr (!DMA) {
@@ -907,13 +905,6 @@ __global__ __launch_bounds__(512, 2) void product_groups_kernel(ProdArgs a, int 
 // ---------------------------------------------------------------------------
 // Launches.
 // ---------------------------------------------------------------------------
-constexpr int64_t CUS = 256;
-
-static int64_t ceil_div(int64_t a, int64_t b)
-{
-    return (a + b - 1) / b;
-}
-
 // row tiles of bt rows: exact, or an upper bound for groups of unknown sizes
 static int64_t row_tiles(const ProdArgs &a, bool grouped, int bt)
 {
@@ -949,195 +940,37 @@ static void launch_groups(const ProdArgs &a, hipStream_t st)
     launch(product_groups_kernel<MODE, OT, DMA>, (unsigned)ceil_div(tt * tn, 8) * 8, 512, 0, st, a, tn);
 }
 
-// rows that the load unit can copy into LDS: on 4 bytes, and within reach
-static bool copies_rows(const ProdArgs &a)
-{
-    return ops_aligned(a.x, 4) && ops_aligned(a.w, 4) && a.ldx % 4 == 0 && a.ldw % 4 == 0 && a.w_stride % 4 == 0 &&
-           a.ldw <= NEAR / 256 && a.ldx <= NEAR / (a.rows ? a.R : 256);
-}
-
-// A tile's time: of a stage, of the rest, and what is added to a stage where the last
-// round has a CU alone with one block.  Fitted to the times above and some 20 more.
-struct TileCost {
-    int bt, bn;
-    double stage, fixed, alone;                      // us
+// products_choice.h's rule with these launches
+template <typename OT, bool GROUPED>
+struct Launches {
+    const ProdArgs &a;
+    hipStream_t st;
+    template <int MODE, bool NT, int RT, int TC, int W>
+    void stream()
+    {
+        launch_stream<MODE, OT, GROUPED, NT, RT, TC, W>(a, st);
+    }
+    template <int MODE, bool DMA, int NB, int WT, int WN, int FT, int FN>
+    void tiles()
+    {
+        launch_tiles<MODE, OT, GROUPED, DMA, NB, WT, WN, FT, FN>(a, st);
+    }
+    template <int MODE, bool DMA>
+    void groups()
+    {
+        launch_groups<MODE, OT, DMA>(a, st);
+    }
 };
 
-// The tile whose rounds over the CUs cost least.
-template <size_t N>
-static int cheapest(const TileCost (&c)[N], const ProdArgs &a)
+template <int MODE, int TILE_MODE, typename OT, bool GROUPED>
+static void enqueue(const ProdArgs &a, hipStream_t st)
 {
-    int best = 0;
-    double least = 0.0;
-    for (int i = 0; i < (int)N; ++i) {
-        const int64_t n = ceil_div(ceil_div(a.M, c[i].bt) * ceil_div(a.N, c[i].bn), CUS);
-        const double stages = a.K / 128.0;
-        const double cost = n * (c[i].stage * stages + c[i].fixed) + (n % 2 ? c[i].alone * stages : 0.0);
-        if (i == 0 || cost < least) {
-            best = i;
-            least = cost;
-        }
-    }
-    return best;
-}
-
-template <int MODE, typename OT>
-static void enqueue_dense_tiles(const ProdArgs &a, hipStream_t st)
-{
-    // Through registers, a piece crossing words and lines: 333 x 5003 x 2048 with 64x64 / 64x128 / 128x256
-    // 18.0 / 19.0 / 31.1 us, 512 x 6144 x 6144 69.7 / 62.8 / 89, 4096 x 6144 x 6144 493 / 353 / 266 (copied
-    // 140); fp32 outputs 23 / 23 / 46, 80 / 135 / 138 and 567 / 796 / 414.  256x256 has too few registers (477).
-    if (!copies_rows(a)) {
-        if constexpr (MODE == F8) {
-            static constexpr TileCost cost[] = {{64, 64, 0.40, 1.5, 0.25}, {64, 128, 0.60, 2.0, 0.3}, {128, 256, 1.8, 4.0, 0.0}};
-            switch (cheapest(cost, a)) {
-            case 0: launch_tiles<MODE, OT, false, false, 2, 2, 2, 2, 2>(a, st); break;
-            case 1: launch_tiles<MODE, OT, false, false, 2, 2, 4, 2, 2>(a, st); break;
-            default: launch_tiles<MODE, OT, false, false, 2, 2, 4, 4, 4>(a, st); break;
-            }
-        } else {
-            static constexpr TileCost cost[] = {{64, 64, 0.46, 1.5, 0.2}, {128, 256, 2.8, 4.0, 0.0}};
-            if (cheapest(cost, a) == 0)
-                launch_tiles<MODE, OT, false, false, 2, 2, 2, 2, 2>(a, st);
-            else
-                launch_tiles<MODE, OT, false, false, 2, 2, 4, 4, 4>(a, st);
-        }
-        return;
-    }
-    if constexpr (MODE == F8) {
-        static constexpr TileCost cost[] = {{64, 64, 0.253, 1.5, 0.08}, {64, 128, 0.36, 2.2, 0.0}, {128, 128, 0.56, 3.5, 0.0},
-                                            {128, 256, 0.95, 4.0, 0.0}, {256, 256, 1.55, 7.0, 0.0}};
-        switch (cheapest(cost, a)) {
-        case 0: launch_tiles<MODE, OT, false, true, 4, 2, 2, 2, 2>(a, st); break;
-        case 1: launch_tiles<MODE, OT, false, true, 3, 2, 4, 2, 2>(a, st); break;
-        case 2: launch_tiles<MODE, OT, false, true, 3, 4, 2, 2, 4>(a, st); break;
-        case 3: launch_tiles<MODE, OT, false, true, 3, 2, 4, 4, 4>(a, st); break;
-        default: launch_tiles<MODE, OT, false, true, 2, 2, 4, 8, 4>(a, st); break;
-        }
-    } else {
-        static constexpr TileCost cost[] = {{64, 64, 0.305, 1.5, 0.2}, {64, 128, 0.52, 2.5, 0.2}, {128, 128, 1.02, 3.5, 0.0},
-                                            {128, 256, 1.65, 4.0, 0.0}};
-        switch (cheapest(cost, a)) {
-        case 0: launch_tiles<MODE, OT, false, true, 4, 2, 2, 2, 2>(a, st); break;
-        case 1: launch_tiles<MODE, OT, false, true, 3, 2, 4, 2, 2>(a, st); break;
-        case 2: launch_tiles<MODE, OT, false, true, 3, 4, 2, 2, 4>(a, st); break;
-        default: launch_tiles<MODE, OT, false, true, 3, 2, 4, 4, 4>(a, st); break;
-        }
-    }
-}
-
-// Streams as long as their blocks fit the card: a block has its K in W parts at once, where
-// a tile's stages come one after the other at 0.4 us each (64 x 6144 x 6144: stream 11.6 us,
-// tile 20.2; 256 x 2048 x 7168 12.4 and 23.2; 64 x 4096 x 7168 9.0 and 22.9; of fp32
-// 64 x 6144 x 6144 14.7 and 28.8).  With half as many blocks again it is the same
-// (128 x 6144 x 2048 9.3 and 9.0; of fp32 128 x 6144 x 6144 23.3 and 30.4), with more the tiles win
-// (256 x 6144 x 6144 28.3 and 23.2).  Where rows are not copied the tiles take twice as long, the
-// streams half as much again (128 x 6144 x 6144 34.6 and 45.5, 256 rows 50.2 and 47.2; of fp32 256
-// rows 53.4 and 68.5), so they go on to 2 or 3 blocks for each CU.  Smaller blocks while they fit: of 16 channels, 32, then 64 (64 x 4096 x 7168:
-// 12.7, 9.0, 11.7; 48 x 2048 x 7168 of F8X: 7.9, 10.0), of 8 rows if there are no more; 16
-// waves where they alone fill the card (1 x 2048 x 7168 4.5 us, 8 waves 4.8; 1 x 6144 x 6144
-// 8.0 and 7.0).  Up to 32 rows all are streams (32 x 24576 x 6144 24.8, tiles 24.6; 32 x 8192 x
-// 7168 11.5 and 24.2).
-template <int MODE, int TILE_MODE, typename OT>
-static void enqueue_dense(const ProdArgs &a, hipStream_t st)
-{
-    const auto blocks = [&](int t, int n) { return ceil_div(a.M, t) * ceil_div(a.N, n); };
-    if (a.M <= 8) {
-        if (blocks(8, 16) <= CUS)
-            launch_stream<MODE, OT, false, false, 1, 1, 16>(a, st);
-        else
-            launch_stream<MODE, OT, false, false, 1, 1, 8>(a, st);
-    } else if (a.M <= 16) {
-        if (blocks(16, 16) <= CUS)
-            launch_stream<MODE, OT, false, false, 1, 2, 8>(a, st);
-        else
-            launch_stream<MODE, OT, false, false, 2, 2, 8>(a, st);
-    } else if (a.M <= 32) {
-        if (blocks(32, 16) <= CUS)
-            launch_stream<MODE, OT, false, false, 1, 4, 8>(a, st);
-        else if (blocks(32, 32) <= CUS)
-            launch_stream<MODE, OT, false, false, 2, 4, 8>(a, st);
-        else
-            launch_stream<MODE, OT, false, false, 2, 4, 4>(a, st);
-    } else if (blocks(32, 16) <= CUS) {
-        launch_stream<TILE_MODE, OT, false, false, 1, 4, 8>(a, st);
-    } else if (blocks(32, 32) <= CUS) {
-        launch_stream<TILE_MODE, OT, false, false, 2, 4, 8>(a, st);
-    } else if (2 * blocks(32, 64) <= CUS * (copies_rows(a) ? (TILE_MODE == F8 ? 2 : 3) : (TILE_MODE == F8 ? 4 : 6))) {
-        launch_stream<TILE_MODE, OT, false, false, 4, 4, 4>(a, st);
-    } else {
-        enqueue_dense_tiles<TILE_MODE, OT>(a, st);
-    }
-}
-
-// Few blocks in all, as a router's logits are: whatever the groups' sizes, K in eight parts.
-// 64 rows in 2 groups of 256 x 6144 of bf16 6.2 us (tiles 32, 16-row streams 8.9), 128 rows 6.9 in
-// blocks of 16 rows and 8.7 of 8, 1000 rows 14.5 (tiles 34); 100 x 4 of 8 of 512 x 4096
-// 7.8 (tiles 16.8).  False where there are more.
-template <int MODE, typename OT>
-static bool enqueue_few(const ProdArgs &a, int64_t rows, hipStream_t st)
-{
-    const auto blocks = [&](int t, int n) { return (a.E < a.M ? a.E : a.M) * ceil_div(rows, t) * ceil_div(a.N, n); };
-    if (blocks(8, 16) <= CUS / 2)
-        launch_stream<MODE, OT, true, false, 1, 1, 8>(a, st);
-    else if (blocks(16, 16) <= CUS)
-        launch_stream<MODE, OT, true, false, 1, 2, 8>(a, st);
-    else if (blocks(32, 32) <= CUS)
-        launch_stream<MODE, OT, true, false, 2, 4, 8>(a, st);
+    const ProductSizes sizes{a.M, a.N, a.K, a.E, copies_rows(a.x, a.w, a.ldx, a.ldw, a.w_stride, a.rows ? a.R : 0)};
+    Launches<OT, GROUPED> launch{a, st};
+    if constexpr (GROUPED)
+        choose_grouped<MODE, TILE_MODE>(sizes, launch);
     else
-        return false;
-    return true;
-}
-
-// By the rows of a group on average.  Streams up to 12 (24 where tiles have the bf16 unit too):
-// E4M3, 64 experts of 2048 x 2048 with 16 rows each 44.9 us and tiles 41.5, of bf16 105.8 and
-// 114.5, 24 rows 115 and 123, 32 rows 117.6 and 117.0.  Weights that pass the caches are read
-// so too: 256 of 4096 x 6144 by 16 tokens x 8 280 us and 317, by 256 tokens 897 and 938;
-// where they stay in them not: 64 of 2048 x 2048 by 64 tokens 48 and 40.
-// Tiles: 64 x 128 below 24 rows (bf16 64: 125 rows 157 us, groups' tiles 151, 32 rows
-// 116 and 146) and where the groups' do not fill the card (16 experts of 2048 x 4096, 64 rows each
-// 28 us, groups' 47; 512 rows each 125 and 107).  F8X: 64 x 128 below 128 rows (125
-// rows 123 us, 128 x 256 136; 512 rows 402 and 312).  Rows that are not copied (64 experts of
-// 2048 x 2048): E4M3 64 x 128 below 256 rows (125 rows 160 us, 128 x 256 170; 512 rows 481 and 373); on
-// the bf16 unit streams up to 64 (32 rows 97, 128 x 256 123; 64 rows 167 and 181; of bf16 236 and the
-// groups' tiles 277), then F8X 128 x 256, bf16 the groups' tiles (125 rows 290, 128 x 256 338).
-template <int MODE, int TILE_MODE, typename OT>
-static void enqueue_grouped(const ProdArgs &a, hipStream_t st)
-{
-    const int64_t rows = ceil_div(a.M, a.E);
-    if (rows <= 12 ? enqueue_few<MODE, OT>(a, rows, st) : enqueue_few<TILE_MODE, OT>(a, rows, st))
-        return;
-    // weights that the last-level cache does not keep from one call to the next, and
-    // that hardly anyone reads twice
-    const bool passing = (int64_t)(a.E < a.M ? a.E : a.M) * a.N * a.K >= (512ll << 20);
-    if (rows <= 4) {
-        if (passing)
-            launch_stream<MODE, OT, true, true, 2, 2, 4>(a, st);
-        else
-            launch_stream<MODE, OT, true, false, 2, 2, 4>(a, st);
-    } else if (rows <= (TILE_MODE == F8 ? 12 : copies_rows(a) ? 24 : 64)) {
-        if (passing && rows <= 12)
-            launch_stream<MODE, OT, true, true, 4, 4, 4>(a, st);
-        else
-            launch_stream<MODE, OT, true, false, 4, 4, 4>(a, st);
-    } else if (!copies_rows(a)) {
-        if constexpr (TILE_MODE == BF16)
-            launch_groups<BF16, OT, false>(a, st);
-        else if (TILE_MODE == F8 && rows < 256)
-            launch_tiles<TILE_MODE, OT, true, false, 2, 2, 4, 2, 2>(a, st);
-        else
-            launch_tiles<TILE_MODE, OT, true, false, 2, 2, 4, 4, 4>(a, st);
-    } else if constexpr (TILE_MODE == F8X) {
-        if (rows < 128)
-            launch_tiles<F8X, OT, true, true, 3, 2, 4, 2, 2>(a, st);
-        else
-            launch_tiles<F8X, OT, true, true, 3, 2, 4, 4, 4>(a, st);
-    } else {
-        if (rows < (TILE_MODE == BF16 ? 64 : 24) || a.E * ceil_div(rows, 256) * ceil_div(a.N, 256) < CUS)
-            launch_tiles<TILE_MODE, OT, true, true, 3, 2, 4, 2, 2>(a, st);
-        else
-            launch_groups<TILE_MODE, OT, true>(a, st);
-    }
+        choose_dense<MODE, TILE_MODE>(sizes, launch);
 }
 
 static moe_status check_product(int32_t N, int32_t n_max, int32_t K, int32_t out_dtype)
@@ -1190,9 +1023,9 @@ extern "C" moe_status moe_linear_fp8(const void *q, int64_t ldq, const float *s,
     const ProdArgs a{static_cast<const uint8_t *>(q), static_cast<const uint8_t *>(w), s, ws, bias, out,
                      nullptr, nullptr, ldq, ldw, 0, lds, ldws, 0, ldo, T, T, N, 1, K};
     if (out_dtype == MOE_DT_F32)
-        enqueue_dense<F8X, F8X, float>(a, static_cast<hipStream_t>(stream));
+        enqueue<F8X, F8X, float, false>(a, static_cast<hipStream_t>(stream));
     else
-        enqueue_dense<F8X, F8, bf16_t>(a, static_cast<hipStream_t>(stream));
+        enqueue<F8X, F8, bf16_t, false>(a, static_cast<hipStream_t>(stream));
     return launched("E4M3 product launch");
 }
 
@@ -1239,12 +1072,12 @@ extern "C" moe_status moe_grouped_linear(const void *x, int32_t x_dtype, int64_t
                      (int)(K * b)};
     hipStream_t hs = static_cast<hipStream_t>(stream);
     if (f8 && out_dtype == MOE_DT_F32)
-        enqueue_grouped<F8X, F8X, float>(a, hs);
+        enqueue<F8X, F8X, float, true>(a, hs);
     else if (f8)
-        enqueue_grouped<F8X, F8, bf16_t>(a, hs);
+        enqueue<F8X, F8, bf16_t, true>(a, hs);
     else if (out_dtype == MOE_DT_F32)
-        enqueue_grouped<BF16, BF16, float>(a, hs);
+        enqueue<BF16, BF16, float, true>(a, hs);
     else
-        enqueue_grouped<BF16, BF16, bf16_t>(a, hs);
+        enqueue<BF16, BF16, bf16_t, true>(a, hs);
     return launched("grouped product launch");
 }

@@ -6,14 +6,15 @@
 
 namespace moe {
 
-// The memory of a copy that takes bytes [at, ...) of each row, of rows that end `end` bytes
-// past the first one's beginning: it begins at `at` itself and has this many bytes, so
-// that a lane's offset alone says whether it is inside.  (The stage as a scalar
-// offset would rest on how the unit's check takes that into account, and on a difference
-// that must not wrap where nothing is left.)
-constexpr uint32_t window_bytes(uint32_t end, uint32_t at)
+// The memory of a copy that takes bytes [at, ...) of each row, of rows that are `row` bytes
+// long and end `end` >= row bytes past the first one's beginning: it begins at `at`
+// itself and has this many bytes, none where it begins past a row's end, so that a lane's
+// offset alone says whether it is inside.  (The stage as a scalar offset would rest on how
+// the unit's check takes that into account, and on a difference that must not wrap where
+// nothing is left.)
+constexpr uint32_t window_bytes(uint32_t end, int at, int row)
 {
-    return at < end ? end - at : 0u;
+    return at < row ? end - (uint32_t)at : 0u;
 }
 
 }  // namespace moe

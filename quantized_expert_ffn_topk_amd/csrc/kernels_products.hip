@@ -593,8 +593,8 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     v4i reg[DMA ? 1 : CP];
     auto fetch = [&](int i, int buf, int st) INLINE {    // sets out copy i of stage st
         if constexpr (DMA) {                         // past the last stage from 0 bytes: zeros, nothing is read
-            const uint32_t at = 128 * (uint32_t)st, end = i < TP ? x_end : w_end;
-            copy16(buffer_of((i < TP ? x0 : w0) + at, st < stages ? window_bytes(end, at) : 0u), lane_at[i], lds0 + buf + lds_at(i));
+            const int at = 128 * st;
+            copy16(buffer_of((i < TP ? x0 : w0) + at, window_bytes(i < TP ? x_end : w_end, at, a.K)), lane_at[i], lds0 + buf + lds_at(i));
         } else if ((a.K & 127) && st >= stages - 1) {
             reg[i] = load_piece_end(src[i] - 16 * piece, 128 * (stages - 1) + 16 * piece, a.K);
         } else {
@@ -638,7 +638,7 @@ __device__ __forceinline__ void tile_product(const ProdArgs &a, const Tile &t, u
     }
     auto bring = [&](int q) INLINE {                 // sets out a quad's copy
         if (SCALED && 64 * wave < BT && 4 * q < stages)
-            copy16(buffer_of(s_first + 16 * q, window_bytes(s_end, 16 * (uint32_t)q)), s_lane,
+            copy16(buffer_of(s_first + 16 * q, window_bytes(s_end, 16 * q, 4 * stages)), s_lane,
                    lds0 + S::TSCALE + 16 * (SROWS * (q & 1) + 64 * wave));
     };
 

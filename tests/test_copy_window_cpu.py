@@ -27,12 +27,12 @@ def test_copies_have_no_scalar_offset():
 def window(tmp_path_factory):
     d = tmp_path_factory.mktemp("window")
     source, lib = d / "w.cpp", d / "w.so"
-    source.write_text('#include "copy_window.h"\nextern "C" uint32_t window(uint32_t end, uint32_t at)\n'
-                      "{\n    return moe::window_bytes(end, at);\n}\n")
+    source.write_text('#include "copy_window.h"\nextern "C" uint32_t window(uint32_t end, int at, int row)\n'
+                      "{\n    return moe::window_bytes(end, at, row);\n}\n")
     subprocess.run(build.CXX.split() + ["-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + CSRC, str(source), "-o", str(lib)],
                    check=True)
     f = C.CDLL(str(lib)).window
-    f.argtypes, f.restype = [C.c_uint32] * 2, C.c_uint32
+    f.argtypes, f.restype = [C.c_uint32, C.c_int, C.c_int], C.c_uint32
     return f
 
 
@@ -43,18 +43,19 @@ def test_a_word_is_read_where_it_is_inside_and_nowhere_else(window, rows, ld, K)
     """Stage st of a row's piece at lane offset r*ld + 16*c, word by word: read if all of it lies in the buffer."""
     end = ((rows - 1) * ld + K + 3) & ~3
     assert end < 1 << 32
-    for st in sorted({0, 1, (K - 1) // 128, (K - 1) // 128 + 1, end // 128, end // 128 + 1}):
+    for st in sorted({0, 1, (K - 1) // 128, (K - 1) // 128 + 1, (K - 1) // 128 + 4, end // 128 + 1}):
         at = 128 * st
-        size = window(end, at)
-        assert at + size <= max(end, at) and size == max(0, end - at)
+        size = window(end, at, K)
+        assert size == (end - at if at < K else 0)               # stages behind a row's last take nothing
         for r in {0, rows // 2, rows - 1}:
             for w in range(32):
                 off = r * ld + 4 * w
                 read = off + 4 <= size
-                assert read == (at + off + 4 <= end)             # no word behind the last row's
+                assert not read or at + off + 4 <= end           # no word behind the last row's
                 assert read or at + 4 * w >= K                   # and none of a row's own is missing
 
 
 def test_nothing_is_read_where_nothing_is_left(window):
-    for end, at in ((0, 0), (4, 4), (4, 128), (128, 256), (0, (1 << 32) - 1), ((1 << 31) + 4, 1 << 31), (1 << 31, (1 << 31) + 4)):
-        assert window(end, at) == max(0, end - at)
+    for end, at, row in ((4, 0, 0), (4, 4, 4), (4, 128, 1), (128, 256, 128), (1 << 31, 1 << 17, 1 << 17), (1 << 31, (1 << 17) + 128, 1 << 17)):
+        assert window(end, at, row) == 0
+    assert window((1 << 31) + 4, 0, 1 << 18) == (1 << 31) + 4 and window(1 << 31, 128, 129) == (1 << 31) - 128

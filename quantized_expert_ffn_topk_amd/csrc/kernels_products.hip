@@ -225,11 +225,13 @@ __device__ __forceinline__ v4i buffer_of(const uint8_t *p, uint32_t bytes)
 // scalar offset is 0: what the unit checks is the lane's offset against the size.
 // In assembly: told of copies into LDS, the compiler waits for those on their way
 // before it reads LDS elsewhere, unless it can tell the places apart; here the
-// callers wait.  (m0 is the compiler's, and kept.)
+// callers wait.  (m0 is the compiler's, and kept.)  The descriptor may have come out of
+// vector registers just before: a memory instruction reads such a scalar 5 wait
+// states later at the earliest, which the compiler does not see to inside assembly.
 __device__ __forceinline__ void copy16(v4i from, uint32_t lane_at, int to)
 {
     int m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\t"
                  "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0)
                  : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(lane_at), "s"(from)

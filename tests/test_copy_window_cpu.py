@@ -23,6 +23,25 @@ def test_copies_have_no_scalar_offset():
     assert seen == 1
 
 
+def wait_states(instructions):
+    """Of instructions one after the other: one each, s_nop n another n."""
+    return sum(1 + (int(i.split()[1]) if i.startswith("s_nop") else 0) for i in instructions)
+
+
+def test_copies_wait_for_a_descriptor_that_came_out_of_vector_registers():
+    """5 wait states between a vector instruction that writes a scalar register and a memory instruction that reads
+    it; the compiler puts them in where it knows the memory instruction, not in front of assembly."""
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(CSRC, "*"))):
+        for body in re.findall(r"asm volatile\((.*?)\n\s*:", open(path).read(), re.S):
+            code = "".join(re.findall(r'"([^"]*)"', body)).split("\\n\\t")
+            loads = [i for i, c in enumerate(code) if re.match(r"buffer_(load|store|atomic)", c)]
+            for i in loads:
+                seen += 1
+                assert wait_states(code[:i]) >= 5, (os.path.basename(path), code)
+    assert seen == 1
+
+
 @pytest.fixture(scope="module")
 def window(tmp_path_factory):
     d = tmp_path_factory.mktemp("window")

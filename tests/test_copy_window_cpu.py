@@ -59,22 +59,24 @@ def window(tmp_path_factory):
 @pytest.mark.parametrize("rows,ld,K", [(1, 4, 1), (1, 128, 128), (3, 132, 129), (5, 300, 300), (64, 516, 513), (2, 1 << 20, 700),
                                        (256, 1 << 23, 1 << 18)])
 def test_a_word_is_read_where_it_is_inside_and_nowhere_else(window, rows, ld, K):
-    """Stage st of a row's piece at lane offset r*ld + 16*c, word by word: read if all of it lies in the buffer."""
+    """Stage st of a row's piece at lane offset r*ld + 128*st + 16*c, word by word: read if all of it lies in the
+    buffer."""
     end = ((rows - 1) * ld + K + 3) & ~3
     assert end < 1 << 32
     for st in sorted({0, 1, (K - 1) // 128, (K - 1) // 128 + 1, (K - 1) // 128 + 4, end // 128 + 1}):
         at = 128 * st
         size = window(end, at, K)
-        assert size == (end - at if at < K else 0)               # stages behind a row's last take nothing
+        assert size == (end if at < K else 0)                    # stages behind a row's last take nothing
         for r in {0, rows // 2, rows - 1}:
             for w in range(32):
-                off = r * ld + 4 * w
+                off = r * ld + at + 4 * w
+                assert off + 4 < 1 << 32 or size == 0
                 read = off + 4 <= size
-                assert not read or at + off + 4 <= end           # no word behind the last row's
+                assert not read or off + 4 <= end                # no word behind the last row's
                 assert read or at + 4 * w >= K                   # and none of a row's own is missing
 
 
 def test_nothing_is_read_where_nothing_is_left(window):
-    for end, at, row in ((4, 0, 0), (4, 4, 4), (4, 128, 1), (128, 256, 128), (1 << 31, 1 << 17, 1 << 17), (1 << 31, (1 << 17) + 128, 1 << 17)):
+    for end, at, row in ((4, 4, 4), (4, 128, 1), (128, 256, 128), (1 << 31, 1 << 17, 1 << 17), (1 << 31, (1 << 17) + 128, 1 << 17)):
         assert window(end, at, row) == 0
-    assert window((1 << 31) + 4, 0, 1 << 18) == (1 << 31) + 4 and window(1 << 31, 128, 129) == (1 << 31) - 128
+    assert window((1 << 31) + 4, 0, 1 << 18) == (1 << 31) + 4 and window(1 << 31, 128, 129) == 1 << 31

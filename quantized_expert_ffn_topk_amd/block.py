@@ -380,6 +380,8 @@ class Fp8MoEFFN(_Norm):
                                    self.s_dn, fb, hb * fb, H, F, self.yr, abi.DT_BF16, H, stream)
             if self.shared is not None:
                 self.shared.products(T, self.q, self.s, out, stream)
+            # the shared expert's rows are of out's type: a bf16 output rounds them once more (2^-8 of
+            # them at most, as its own rounding), an fp32 one does not
             abi.moe_combine_rows(self.yr, abi.DT_BF16, H, M, self.pos, self.w, out if self.shared is not None else None, H, T, k, H,
                                  out, _dtype(out), H, stream)
         return out, h

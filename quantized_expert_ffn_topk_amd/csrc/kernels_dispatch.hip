@@ -17,10 +17,9 @@ struct GroupArgs {
 // has a run of neighbouring ids, 64 at a time, so its list follows those of the
 // waves before it.  Bound by the instructions of all blocks' rounds (E*M/64 in all):
 // two comparisons each, no bounds in whole batches, more only where an id is found.
-// In a graph 16 x 8 of 256 2.5 us, a launch; 1024 x 8 3.6; 4096 x 8 5.3; 8192 x 8 8.0.  The
+// In a graph 16 x 8 of 256 3.1 us, a launch; 1024 x 8 3.9; 4096 x 8 5.7; 8192 x 8 8.3.  The
 // three sizes of lists are for what a block's LDS leaves to others and how many loads are worth a
-// batch; the limit is that of a CU's LDS, and above it the three launches below take
-// 28 us for 16384 x 8.
+// batch; the limit is that of a CU's LDS.
 // ---------------------------------------------------------------------------
 constexpr int GROUP_W = 16;                          // waves
 constexpr int GROUP_ONE = 64 * 64 * GROUP_W;         // ids of one launch
@@ -96,7 +95,9 @@ __global__ __launch_bounds__(64 * GROUP_W) void group_rows_kernel(GroupArgs a)
 // More ids, in three launches: the counts of each run of GROUP_RUN ids, their
 // sums over the runs, and each run's ids by these.  The counts of a run lie at the
 // beginning of its own part of pos until the last step takes them out and writes
-// pos itself (a run is longer than the experts are many).
+// pos itself (a run is longer than the experts are many).  27 us for 66048 ids of 256
+// experts, 28 for 131072, 47 for 2^20: not the launches but few long runs (4 blocks, 8, 64) that each
+// walk their ids twice in 16 rounds or more, and one block that adds up the runs.
 // ---------------------------------------------------------------------------
 constexpr int GROUP_RUN = 16384;
 constexpr int MAX_E = 1024;
@@ -214,7 +215,8 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int runs
 // out[t] = base[t] + sum_i w[t,i] * y[pos[t,i]], fp32 FMAs in the order of i,
 // rounded once.  A thread has eight columns of a token; the loads of eight of
 // its rows are in flight at once.  Bound by HBM: 4096 x 8 x 6144 with base 98 us (5.1 TB/s);
-// 1 x 8 x 6144 2.9 us in a graph.
+// 1 x 8 x 6144 3.1 us in a graph.  Columns behind the last eight are one thread's, row after row:
+// 1 x 8 x 6143 10.5 us, 4096 x 8 x 6143 144.
 // ---------------------------------------------------------------------------
 struct CombineArgs {
     const void *y, *base;

@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t row16_top(uint32_t v)
 // ---------------------------------------------------------------------------
 // 16 lanes per block of 128, eight values a lane (16 bytes of bf16), the blocks of all
 // rows in one count: one pass, no LDS, the maximum by four lane rotations.  Bound by
-// HBM: SwiGLU of 32768 x 2048 63 us (6.4 TB/s read and written), 4096 x 6144 14.5 us;
-// one row of 6144 2.0 us in a graph, a launch.
+// HBM: SwiGLU of 32768 x 2048 63 us (5.4 TB/s read and written), 4096 x 6144 14.9 us;
+// one row of 6144 2.2 us in a graph, a launch.
 // ---------------------------------------------------------------------------
 template <typename XT, bool SWIGLU>
 __global__ __launch_bounds__(256) void quant_fp8_kernel(Fp8Args a, int blocks)

@@ -329,7 +329,7 @@ __device__ __forceinline__ void add_stage(v4f &acc, const Frag<MODE> &w, const F
 // stage comes.
 // Bytes on their way are what counts: a row of 6144 x 6144 7.0 us (5.4 TB/s) with 8 waves
 // of 16 rows, 24576 x 6144 23.1 (6.5); 16 tokens to 8 each of 256 experts of
-// 4096 x 6144 280 us.
+// 4096 x 6144 (some 80 have rows) 281 to 297, by card.
 // ---------------------------------------------------------------------------
 template <int MODE, typename OT, bool GROUPED, bool NT, int RT, int TC, int W>
 __global__ __launch_bounds__(64 * W, 2) void product_stream_kernel(ProdArgs a, int tiles_n)
@@ -506,25 +506,29 @@ __global__ __launch_bounds__(64 * W, 2) void product_stream_kernel(ProdArgs a, i
 // come four stages at a time (16 bytes of a row of scales; one by one they would
 // be a line each) into one of two places while the other is read.
 // A partial last stage comes by the same copies and is cleared in LDS past the rows'
-// end before it is read: 333 x 5003 x 2000 11.6 us, x 2048 11.3.
+// end before it is read: 333 x 5003 x 2000 11.0 us, x 2048 11.2.
 //
-// Measured, in us, for bf16 outputs (F8; tiles of rows x channels):
+// Measured, in us, for bf16 outputs (F8; tiles of rows x channels; 70 shapes are in
+// profiles/e4m3_product_kernels.csv):
 //                        64x64  64x128  128x128  128x256  256x256
-//     64 x  6144 x 6144   19.1    21.1     26.8     38.7     62.9   (streams: 11.6)
-//    333 x  5003 x 2048   10.9    10.1     12.2     17.2     27.8
-//    128 x 24576 x 6144   46.5    37.0     31.8     41.9     64.5
-//    600 x  8192 x 4096   45.2    37.1     39.0     30.7     46.7
-//   4096 x 24576 x 6144   1168     916      794      620      525
+//     64 x  6144 x 6144   21.8    23.1     26.6     41.3     63.3   (streams: 11.9)
+//    333 x  5003 x 2048   11.5    11.2     12.5     18.4     28.2
+//    128 x 24576 x 6144   44.2    36.1     30.2     42.9     65.4
+//    600 x  8192 x 4096   44.0    37.9     38.7     31.3     46.6
+//   4096 x 24576 x 6144   1184     919      810      620      518
 // and for fp32 outputs (F8X):
-//     64 x  6144 x 6144   29.6    38.0     51.1     78.6            (streams: 14.7)
-//    333 x  5003 x 2048   16.5    16.9     21.1     31.6
-//    512 x  6144 x 6144   63.2    62.5     52.9     79.7
-//    600 x  8192 x 4096   66.2    63.2     70.0     56.8
-//   4096 x 12288 x 6144    773     654      612      506
-// 525 us are 2360 TFLOP/s, the unit 57 % busy at the 1.9 GHz that the card holds under
+//     64 x  6144 x 6144   28.4    37.6     52.7     79.2            (streams: 14.2)
+//    333 x  5003 x 2048   17.6    17.9     22.9     32.3
+//    512 x  6144 x 6144   58.6    59.9     54.9     81.3
+//    600 x  8192 x 4096   67.7    64.7     76.5     58.9
+//   4096 x 12288 x 6144    803     691      671      527
+// 518 us are 2390 TFLOP/s, the unit 59 % busy at the 1.9 GHz that the card holds under
 // it: without the copies 17 % less, without the scaling 11 %, without the stores 7 %.
-// F8X's small tiles are bound by the widening, done by each wave for its own
-// fragments; widened once into LDS, the reads of twice the bytes would take as long.
+// The small tiles wait: a stage of the 64 x 64 ones takes 0.45 us, with one wave on a SIMD
+// that reads its fragments from LDS one step ahead of their products.  Of F8X's 17.6 us at
+// 333 x 5003 x 2048 the widening, done by each wave for its own fragments, is some 7
+// (16 stages, two waves on a SIMD, 64 conversions of 7 cycles each); widened once into LDS,
+// the reads of twice the bytes would take as long.
 // ---------------------------------------------------------------------------
 constexpr int MAX_BLOCKS = 1024;                     // blocks of 128 codes in a row
 
@@ -885,8 +889,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void product_tiles_kernel(ProdArgs
 //   1024 tokens x 8 of 256 experts of 4096 x 6144   1185 / 1160 / 1135  (HBM, 5.6 TB/s)
 //   4096 x 8 of 256                                  1931 / 1605 / 1560
 //   4096 x 8 of  64 of 2048 x 2048                    273 /  199 /  176
-// 4096 x 8 of 256 is 1020 us of products and 1030 of weights, which two stages on their way
-// overlap in part: 1165 with all weights in L2.  A third stage has no room in LDS.
+// 4096 x 8 of 256 is 1020 us of products (27 % of them for rows that only fill up tiles) and
+// 1030 of weights, overlapped in part: 1165 with all weights in L2.  On their way are two stages
+// (up to 96 KB) in tiles of 64 and 128 rows, one (56 and 64 KB) in those of 192 and 256, whose
+// third buffer has no room in LDS.
 template <int MODE, typename OT, bool DMA>
 __global__ __launch_bounds__(512, 2) void product_groups_kernel(ProdArgs a, int tiles_n)
 {

@@ -39,7 +39,10 @@ inline bool copies_rows(const void *x, const void *w, int64_t ldx, int64_t ldw, 
 }
 
 // A tile's time: of a stage, of the rest, and what is added to a stage where the last
-// round has a CU alone with one block.  Fitted to the times above and some 20 more.
+// round has a CU alone with one block.  Fitted to the times in kernels_products.hip and some
+// 20 more.  On the 70 shapes of profiles/e4m3_product_kernels.csv the kernel that is taken,
+// streams among them, loses to the fastest one 0.3 % on average and 14 % at most for bf16 outputs, 1.9 and
+// 21 % for fp32; where rows pass through registers 0.7 and 11 %, 2.0 and 22 %.
 struct TileCost {
     int bt, bn;
     double stage, fixed, alone;                      // us
@@ -67,8 +70,8 @@ template <int MODE, typename Launch>
 void choose_dense_tiles(const ProductSizes &a, Launch &launch)
 {
     // Through registers, a piece crossing words and lines: 333 x 5003 x 2048 with 64x64 / 64x128 / 128x256
-    // 18.0 / 19.0 / 31.1 us, 512 x 6144 x 6144 69.7 / 62.8 / 89, 4096 x 6144 x 6144 493 / 353 / 266 (copied
-    // 140); fp32 outputs 23 / 23 / 46, 80 / 135 / 138 and 567 / 796 / 414.  256x256 has too few registers (477).
+    // 18.1 / 19.0 / 30.6 us, 512 x 6144 x 6144 63 / 59 / 89, 4096 x 6144 x 6144 493 / 353 / 266 (copied
+    // 140); fp32 outputs 22 / 23 / 46, 75 / 135 / 138 and 567 / 796 / 414.  256x256 has too few registers (477).
     if (!a.copies) {
         if constexpr (MODE == F8) {
             static constexpr TileCost cost[] = {{64, 64, 0.40, 1.5, 0.25}, {64, 128, 0.60, 2.0, 0.3}, {128, 256, 1.8, 4.0, 0.0}};
@@ -109,13 +112,14 @@ void choose_dense_tiles(const ProductSizes &a, Launch &launch)
 }
 
 // Streams as long as their blocks fit the card: a block has its K in W parts at once, where
-// a tile's stages come one after the other at 0.4 us each (64 x 6144 x 6144: stream 11.6 us,
-// tile 20.2; 256 x 2048 x 7168 12.4 and 23.2; 64 x 4096 x 7168 9.0 and 22.9; of fp32
-// 64 x 6144 x 6144 14.7 and 28.8).  With half as many blocks again it is the same
-// (128 x 6144 x 2048 9.3 and 9.0; of fp32 128 x 6144 x 6144 23.3 and 30.4), with more the tiles win
-// (256 x 6144 x 6144 28.3 and 23.2).  Where rows are not copied the tiles take twice as long, the
-// streams half as much again (128 x 6144 x 6144 34.6 and 45.5, 256 rows 50.2 and 47.2; of fp32 256
-// rows 53.4 and 68.5), so they go on to 2 or 3 blocks for each CU.  Smaller blocks while they fit: of 16 channels, 32, then 64 (64 x 4096 x 7168:
+// a tile's stages come one after the other at 0.45 us each (64 x 6144 x 6144: stream 11.9 us,
+// tile 21.8; 256 x 2048 x 7168 12.7 and 24.9; 64 x 4096 x 7168 9.0 and 22.9; of fp32
+// 64 x 6144 x 6144 14.2 and 28.4).  With half as many blocks again they are near each other
+// (128 x 6144 x 2048 9.3 and 9.0; 128 x 6144 x 6144 19.2 and 21.9, of fp32 22.1 and 28.6), with
+// more the tiles win (256 x 6144 x 6144 29.5 and 25.7).  Where rows are not copied the tiles take
+// twice as long, the streams half as much again (128 x 6144 x 6144 32.4 and 44.7, 256 rows 48.3
+// and 46.0; of fp32 256 rows 51.0 and 67.9), so they go on to 2 or 3 blocks for each CU.
+// Smaller blocks while they fit: of 16 channels, 32, then 64 (64 x 4096 x 7168:
 // 12.7, 9.0, 11.7; 48 x 2048 x 7168 of F8X: 7.9, 10.0), of 8 rows if there are no more; 16
 // waves where they alone fill the card (1 x 2048 x 7168 4.5 us, 8 waves 4.8; 1 x 6144 x 6144
 // 8.0 and 7.0).  Up to 32 rows all are streams (32 x 24576 x 6144 24.8, tiles 24.6; 32 x 8192 x
@@ -171,7 +175,8 @@ bool choose_few(const ProductSizes &a, int64_t rows, Launch &launch)
     return true;
 }
 
-// By the rows of a group on average.  Streams up to 12 (24 where tiles have the bf16 unit too):
+// By the rows of a group on average, with borders from weights of 2048 x 2048 and 4096 x 6144.
+// Streams up to 12 (24 where tiles have the bf16 unit too):
 // E4M3, 64 experts of 2048 x 2048 with 16 rows each 44.9 us and tiles 41.5, of bf16 105.8 and
 // 114.5, 24 rows 115 and 123, 32 rows 117.6 and 117.0.  Weights that pass the caches are read
 // so too: 256 of 4096 x 6144 by 16 tokens x 8 280 us and 317, by 256 tokens 897 and 938;
